@@ -61,10 +61,45 @@ class SprHeadStats(ctypes.Structure):
     ]
 
 
+class SprNormRotateParams(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+        ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+        ("qo_strides", ctypes.c_int64 * 3), ("ko_strides", ctypes.c_int64 * 3),
+        ("dtype_in", ctypes.c_int32), ("dtype_out", ctypes.c_int32),
+        ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("rot", ctypes.c_int32), ("pairing", ctypes.c_int32),
+    ]
+
+
+class SprMaskedParams(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+        ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+        ("v_strides", ctypes.c_int64 * 3), ("o_strides", ctypes.c_int64 * 3),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+        ("causal", ctypes.c_int32), ("q_start", ctypes.c_int32),
+    ]
+
+
+class SprProjectParams(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("N", ctypes.c_int32), ("Hx", ctypes.c_int32),
+        ("dx", ctypes.c_int32), ("Hy", ctypes.c_int32), ("dy", ctypes.c_int32),
+        ("x_strides", ctypes.c_int64 * 3), ("y_strides", ctypes.c_int64 * 3),
+        ("r_strides", ctypes.c_int64 * 3), ("w_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+    ]
+
+
 EXPORTS = ["sparsepr_workspace_size", "sparsepr_check_params", "sparsepr_partition",
            "sparsepr_route", "sparsepr_attend", "sparsepr_reconstruct", "sparsepr_call",
            "sparsepr_get_stats", "sparsepr_workspace_view", "sparsepr_version",
-           "sparsepr_launch_count", "sparsepr_attend_routed_noalloc"]
+           "sparsepr_launch_count", "sparsepr_attend_routed_noalloc", "sparsepr_norm_rotate",
+           "sparsepr_attend_masked", "sparsepr_attend_masked_workspace", "sparsepr_project",
+           "sparsepr_project_workspace"]
 
 _lib = None
 
@@ -107,6 +142,18 @@ def load_library(path: str = LIB_PATH):
     lib.sparsepr_attend_routed_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                                    i32, ctypes.c_float, vp, vp, vp]
     lib.sparsepr_attend_routed_noalloc.restype = ctypes.c_int
+    lib.sparsepr_norm_rotate.argtypes = [ctypes.POINTER(SprNormRotateParams)] + [vp] * 6 + \
+        [i32] + [vp] * 6
+    lib.sparsepr_norm_rotate.restype = ctypes.c_int
+    lib.sparsepr_attend_masked.argtypes = [ctypes.POINTER(SprMaskedParams)] + [vp] * 11 + \
+        [sz, vp, vp]
+    lib.sparsepr_attend_masked.restype = ctypes.c_int
+    lib.sparsepr_project.argtypes = [ctypes.POINTER(SprProjectParams)] + [vp] * 7 + [sz, vp, vp]
+    lib.sparsepr_project.restype = ctypes.c_int
+    for name, struct in (("sparsepr_attend_masked_workspace", SprMaskedParams),
+                         ("sparsepr_project_workspace", SprProjectParams)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(struct)]
+        getattr(lib, name).restype = sz
     _lib = lib
     return lib
 
@@ -175,10 +222,20 @@ def sparsepr_check_params(prm: SprParams) -> int:
     return load_library().sparsepr_check_params(ctypes.byref(prm))
 
 
-def alloc_workspace(prm: SprParams, device=None) -> torch.Tensor:
-    n = sparsepr_workspace_size(prm)
-    if n == 0:
-        raise SparsePRError("sparsepr_workspace_size", sparsepr_check_params(prm))
+def alloc_workspace(prm, device=None) -> torch.Tensor:
+    """Workspace for a call, a masked attention or a projection with these parameters."""
+    if isinstance(prm, SprMaskedParams):
+        n = load_library().sparsepr_attend_masked_workspace(ctypes.byref(prm))
+        if n == 0:
+            raise SparsePRError("sparsepr_attend_masked_workspace", SPR_EINVAL)
+    elif isinstance(prm, SprProjectParams):
+        n = load_library().sparsepr_project_workspace(ctypes.byref(prm))
+        if n == 0:
+            raise SparsePRError("sparsepr_project_workspace", SPR_EINVAL)
+    else:
+        n = sparsepr_workspace_size(prm)
+        if n == 0:
+            raise SparsePRError("sparsepr_workspace_size", sparsepr_check_params(prm))
     ws = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
     off = (-ws.data_ptr()) % 256
     return ws[off:off + n]

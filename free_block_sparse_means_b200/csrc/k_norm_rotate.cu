@@ -1,0 +1,268 @@
+// RMS norm of the queries and keys of each head with the rotary position
+// embedding in the same pass (sparsepr_norm_rotate in include/sparsepr.h).
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w,  (a, b) -> (a cos - b sin, a sin + b cos)
+//
+// A row is held by LPR lanes of a warp, 8 channels (one 16-byte vector of a
+// 16-bit type) each: the mean is a butterfly over those lanes, interleaved
+// pairs turn inside a lane, and split halves fetch their partner's 8 channels
+// from the lane rot / 16 away.  Everything between the load and the one
+// rounding at the store is fp32.
+#include <cuda_fp16.h>
+
+#include "spr_internal.cuh"
+
+namespace spr {
+namespace {
+
+constexpr int NR_THREADS = 256;
+
+struct NrSide {
+  const void* x;
+  void* y;
+  const void* w;
+  const int32_t* pos;
+  int64_t xs[3], ys[3];
+  int H, N;
+};
+struct NrArgs {
+  NrSide side[2];  // 0 queries, 1 keys
+  const float *cos, *sin;
+  int32_t* status;
+  float eps, inv_d;
+  int B, d, rot, halves, norm, table_rows, heads_per_group;
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f);
+template <>
+__device__ __forceinline__ void load8<bf16>(const bf16* p, float* f) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<__half>(const __half* p, float* f) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    f[2 * i] = g.x;
+    f[2 * i + 1] = g.y;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float* f) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void store8(bf16* p, const float* f) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                            pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+__device__ __forceinline__ void store8(__half* p, const float* f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float* f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Grid: x tiles of tokens, y groups of heads, z = batch and side.
+template <typename TI, typename TO, int LPR>
+__global__ void __launch_bounds__(NR_THREADS) k_norm_rotate(const __grid_constant__ NrArgs a) {
+  const int b = blockIdx.z >> 1;
+  const NrSide& s = a.side[blockIdx.z & 1];
+  const int h0 = blockIdx.y * a.heads_per_group, h1 = min(s.H, h0 + a.heads_per_group);
+  const int l = threadIdx.x % LPR, c0 = 8 * l;  // this lane's channels c0 .. c0 + 7
+  const int n = blockIdx.x * (NR_THREADS / LPR) + threadIdx.x / LPR;
+  if (h0 >= s.H) return;
+  // lanes without a row or channels stay for the shuffles
+  bool live = n < s.N;
+  const bool mine = c0 < a.d;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+  const int half = a.rot >> 1;
+  if (live && a.rot) {
+    const int row = s.pos ? s.pos[(int64_t)b * s.N + n] : n;
+    if (row < 0 || row >= a.table_rows) {
+      if (a.status && l == 0 && h0 == 0 && atomicCAS(a.status, 0, (int)ERR_INDEX) == 0) {
+        a.status[1] = b;
+        a.status[2] = n;
+        a.status[3] = row;
+      }
+      live = false;
+    } else if (c0 < a.rot) {
+      if (a.halves) {  // channel c uses pair c mod rot / 2
+        const int64_t at = (int64_t)row * half + (c0 < half ? c0 : c0 - half);
+        load8(a.cos + at, cs);
+        load8(a.sin + at, sn);
+      } else {  // channels c0 .. c0 + 7 are pairs c0 / 2 .. c0 / 2 + 3
+        const int64_t at = (int64_t)row * half + (c0 >> 1);
+        const float4 c = *reinterpret_cast<const float4*>(a.cos + at);
+        const float4 d = *reinterpret_cast<const float4*>(a.sin + at);
+        cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+        sn[0] = d.x; sn[1] = d.y; sn[2] = d.z; sn[3] = d.w;
+      }
+    }
+  }
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  if (s.w && mine) load8(static_cast<const TI*>(s.w) + c0, w);
+  const bool turned = c0 < a.rot, low = c0 < half;
+  const int partner = low ? (threadIdx.x & 31) + half / 8 : (threadIdx.x & 31) - half / 8;
+  const TI* x = static_cast<const TI*>(s.x) + b * s.xs[0] + (int64_t)n * s.xs[2] + c0;
+  TO* y = static_cast<TO*>(s.y) + b * s.ys[0] + (int64_t)n * s.ys[2] + c0;
+  for (int h = h0; h < h1; ++h) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    if (live && mine) load8(x + h * s.xs[1], f);
+    if (a.norm) {
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q = fmaf(f[i], f[i], q);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+      const float r = rsqrtf(fmaf(q, a.inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+    }
+    if (a.rot) {
+      if (a.halves) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float o = __shfl_sync(0xffffffffu, f[i], partner);
+          if (turned) f[i] = low ? f[i] * cs[i] - o * sn[i] : o * sn[i] + f[i] * cs[i];
+        }
+      } else if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = f[2 * i], q = f[2 * i + 1];
+          f[2 * i] = p * cs[i] - q * sn[i];
+          f[2 * i + 1] = p * sn[i] + q * cs[i];
+        }
+      }
+    }
+    if (live && mine) store8(y + h * s.ys[1], f);
+  }
+}
+
+template <typename TI, typename TO>
+cudaError_t launch(const NrArgs& a, cudaStream_t st) {
+  const int lanes = a.d / 8;
+  auto go = [&](auto kern, int lpr) {
+    const int per = NR_THREADS / lpr;
+    const int N = max(a.side[0].N, a.side[1].H ? a.side[1].N : 0);
+    const int H = max(a.side[0].H, a.side[1].H);
+    const dim3 grid((N + per - 1) / per, (H + a.heads_per_group - 1) / a.heads_per_group, 2 * a.B);
+    spr_launch(kern, grid, NR_THREADS, 0, st, a);
+    return cudaGetLastError();
+  };
+  if (lanes > 16) return go(k_norm_rotate<TI, TO, 32>, 32);
+  if (lanes > 8) return go(k_norm_rotate<TI, TO, 16>, 16);
+  if (lanes > 4) return go(k_norm_rotate<TI, TO, 8>, 8);
+  return go(k_norm_rotate<TI, TO, 4>, 4);
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Rows on 16 bytes: strides in elements, a multiple of `per` where the dimension has more than one entry.
+bool side_strides_ok(const int64_t* s, const int* size, int per, bool out) {
+  for (int i = 0; i < 3; ++i) {
+    if (s[i] < 0 || (size[i] > 1 && s[i] % per)) return false;
+    if (out && size[i] > 1 && s[i] == 0) return false;
+  }
+  return true;
+}
+
+}  // namespace
+}  // namespace spr
+
+using namespace spr;
+
+extern "C" spr_status sparsepr_norm_rotate(const spr_norm_rotate_params* p, const void* Q,
+                                           const void* K, const void* wq, const void* wk,
+                                           const float* cos, const float* sin, int32_t table_rows,
+                                           const int32_t* pos_q, const int32_t* pos_k, void* Qo,
+                                           void* Ko, int32_t* status, void* stream) {
+  if (!p || !Q || !Qo) return SPR_EINVAL;
+  const bool keys = p->Hk > 0;
+  if (p->B < 1 || p->Hq < 1 || p->Hk < 0 || p->Nq < 1 || (keys && p->Nk < 1)) return SPR_EINVAL;
+  if (keys && (!K || !Ko)) return SPR_EINVAL;
+  if (p->dtype_in < SPR_BF16 || p->dtype_in > SPR_FP32 || p->dtype_out < SPR_BF16 ||
+      p->dtype_out > SPR_FP32)
+    return SPR_EINVAL;
+  if (p->dtype_out != p->dtype_in && p->dtype_out != SPR_BF16) return SPR_EUNSUPPORTED;
+  if (p->d < 1 || p->rot < 0 || p->rot > p->d) return SPR_EINVAL;
+  if (p->d % 8 || p->d > 256) return SPR_EUNSUPPORTED;
+  if (p->pairing != SPR_PAIR_INTERLEAVED && p->pairing != SPR_PAIR_HALVES) return SPR_EINVAL;
+  if (p->rot % (p->pairing == SPR_PAIR_HALVES ? 16 : 8)) return SPR_EUNSUPPORTED;
+  if ((p->norm != 0 && p->norm != 1) || !(p->eps >= 0.f) || !isfinite(p->eps)) return SPR_EINVAL;
+  if (!p->norm && (wq || (keys && wk))) return SPR_EINVAL;
+  if (p->rot) {
+    if (!cos || !sin || table_rows < 1) return SPR_EINVAL;
+    if ((!pos_q && p->Nq > table_rows) || (keys && !pos_k && p->Nk > table_rows))
+      return SPR_EINVAL;
+    if (!aligned(cos, 16) || !aligned(sin, 16)) return SPR_EUNSUPPORTED;
+  }
+  if (p->B > 32767 || p->Hq > 65535 || p->Hk > 65535) return SPR_EUNSUPPORTED;
+  const int nq[3] = {p->B, p->Hq, p->Nq}, nk[3] = {p->B, p->Hk, p->Nk};
+  const int pi = p->dtype_in == SPR_FP32 ? 4 : 8, po = p->dtype_out == SPR_FP32 ? 4 : 8;
+  if (!side_strides_ok(p->q_strides, nq, pi, false) || !side_strides_ok(p->qo_strides, nq, po, true))
+    return SPR_EUNSUPPORTED;
+  if (keys && (!side_strides_ok(p->k_strides, nk, pi, false) ||
+               !side_strides_ok(p->ko_strides, nk, po, true)))
+    return SPR_EUNSUPPORTED;
+  if (!aligned(Q, 16) || !aligned(Qo, 16) || !aligned(wq, 16) ||
+      (keys && (!aligned(K, 16) || !aligned(Ko, 16) || !aligned(wk, 16))) || !aligned(pos_q, 4) ||
+      !aligned(pos_k, 4) || !aligned(status, 4))
+    return SPR_EUNSUPPORTED;
+
+  NrArgs a{};
+  a.side[0] = {Q, Qo, wq, pos_q, {}, {}, p->Hq, p->Nq};
+  if (keys) a.side[1] = {K, Ko, wk, pos_k, {}, {}, p->Hk, p->Nk};
+  for (int i = 0; i < 3; ++i) {
+    a.side[0].xs[i] = p->q_strides[i];
+    a.side[0].ys[i] = p->qo_strides[i];
+    a.side[1].xs[i] = p->k_strides[i];
+    a.side[1].ys[i] = p->ko_strides[i];
+  }
+  a.cos = cos;
+  a.sin = sin;
+  a.status = status;
+  a.eps = p->eps;
+  a.inv_d = 1.f / (float)p->d;
+  a.B = p->B;
+  a.d = p->d;
+  a.rot = p->rot;
+  a.halves = p->pairing == SPR_PAIR_HALVES;
+  a.norm = p->norm;
+  a.table_rows = table_rows;
+  a.heads_per_group = 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (status && cudaMemsetAsync(status, 0, 4 * sizeof(int32_t), st) != cudaSuccess)
+    return SPR_ECUDA;
+  cudaError_t e;
+  if (p->dtype_in == SPR_BF16)
+    e = launch<bf16, bf16>(a, st);
+  else if (p->dtype_in == SPR_FP16)
+    e = p->dtype_out == SPR_FP16 ? launch<__half, __half>(a, st) : launch<__half, bf16>(a, st);
+  else
+    e = p->dtype_out == SPR_FP32 ? launch<float, float>(a, st) : launch<float, bf16>(a, st);
+  return e == cudaSuccess ? SPR_OK : SPR_ECUDA;
+}

@@ -338,6 +338,129 @@ spr_status sparsepr_attend_routed_noalloc(const void* Qp, const void* Kp, const 
                                           int32_t Gq, int32_t Gk, float scale, float* O,
                                           int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the call.  The models the call stands in make its Q and K
+ * by a norm and a rotation, keep some layers and steps dense, and project in
+ * front of and behind it; these three entry points are those parts, on the
+ * same layouts.  They follow the conventions at the top of this file, and
+ * take two 16-bit types (and, where stated, fp32).  `status` is int32[4] on the
+ * device, or NULL: after the call's kernels, an error code and three info
+ * words (0 = no error; 1 = an index out of range; 4 = a bounded wait gave up).
+ * All are forward only.
+ * ------------------------------------------------------------------------ */
+enum { SPR_BF16 = 0, SPR_FP16 = 1, SPR_FP32 = 2 };
+enum { SPR_PAIR_INTERLEAVED = 0, SPR_PAIR_HALVES = 1 };
+
+/*
+ * RMS norm of each head's queries and keys and the rotary position embedding.
+ * Q is [B, Hq, Nq, d], K [B, Hk, Nk, d] (Hk = 0: no keys; K, Ko, wk, pos_k are
+ * then ignored).  Strides in elements for batch, head, token; the last
+ * dimension is contiguous, every row starts on 16 bytes.  d is a multiple of 8,
+ * 8..256.  dtype_out is dtype_in or SPR_BF16.  rot channels are rotated, 0..d
+ * (0: none): a multiple of 8, or of 16 with SPR_PAIR_HALVES.
+ */
+typedef struct {
+  int32_t B, Hq, Hk, Nq, Nk, d;
+  int64_t q_strides[3], k_strides[3], qo_strides[3], ko_strides[3];
+  int32_t dtype_in, dtype_out;  /* SPR_BF16, SPR_FP16 or SPR_FP32 */
+  int32_t norm;                 /* 1: RMS norm over the d channels, 0: none */
+  float eps;                    /* added to the mean square, >= 0 */
+  int32_t rot;                  /* rotated channels (the first ones) */
+  int32_t pairing;              /* SPR_PAIR_INTERLEAVED: (2i, 2i+1); _HALVES: (i, i+rot/2) */
+} spr_norm_rotate_params;
+
+/*
+ * y = x * rsqrt(mean(x^2) + eps) * w per row, then pair i of the rotated
+ * channels turns by the angle of its row in the tables:
+ * (a, b) -> (a cos - b sin, a sin + b cos).  fp32 arithmetic, one rounding.
+ *   wq, wk      [d] of dtype_in, or NULL (ones); NULL without the norm
+ *   cos, sin    [table_rows, rot / 2] fp32, contiguous, 16-byte aligned
+ *   pos_q, pos_k [B, Nq], [B, Nk] int32 row of the tables of each token, or NULL
+ *               (token n takes row n; Nq and Nk are then at most table_rows).
+ *               A token whose row is outside the tables is not written in any
+ *               head, and status gets {1, batch, token, row} of one of them.
+ * Qo may be Q and Ko may be K (same strides); any other overlap is undefined.
+ */
+spr_status sparsepr_norm_rotate(const spr_norm_rotate_params* prm, const void* Q, const void* K,
+                                const void* wq, const void* wk, const float* cos,
+                                const float* sin, int32_t table_rows, const int32_t* pos_q,
+                                const int32_t* pos_k, void* Qo, void* Ko, int32_t* status,
+                                void* stream);
+
+/* q_start value: each batch's last query sits on its last key. */
+#define SPR_ALIGN_END INT32_MIN
+
+/*
+ * Exact attention under a mask.  Q, O [B, Hq, Nq, d]; K, V [B, Hk, Nk, d] with Hk
+ * a divisor of Hq (query head h reads key head h / (Hq / Hk)); d 64 or 128.
+ * Strides as in spr_params (multiples of 8 elements, rows on 16 bytes; K and V
+ * may have a batch or head stride of 0).
+ */
+typedef struct {
+  int32_t B, Hq, Hk, Nq, Nk, d;
+  int64_t q_strides[3], k_strides[3], v_strides[3], o_strides[3];
+  int32_t dtype;    /* SPR_BF16 or SPR_FP16: Q, K, V and O */
+  float scale;      /* of the scores; <= 0 selects 1/sqrt(d) */
+  float softcap;    /* c > 0: scores become c tanh(x / c); 0: not capped */
+  int32_t causal;   /* 1: query at position p sees keys j <= p (and the prefix) */
+  int32_t q_start;  /* position of query 0, -2^30..2^30, or SPR_ALIGN_END */
+} spr_masked_params;
+
+/* Bytes of workspace a call with these parameters needs (0 on bad params). */
+size_t sparsepr_attend_masked_workspace(const spr_masked_params* prm);
+
+/*
+ * x_ij = cap(scale q_i . k_j) - slope_h |p_i - j|, p_i = q_start + i (with
+ * SPR_ALIGN_END: len_b - Nq + i, len_b the batch's key count).  Query i sees
+ * key j where j < len_b, and with doc_q / doc_k doc_q[i] == doc_k[j] >= 0, and
+ * with causal j <= p_i or j < prefix[b].  O_i = sum_j softmax_j(x_i) v_j over
+ * the visible keys; a row that sees none is 0, with lse = -inf.
+ *   k_len   [B] int32 filled keys of each batch, or NULL (Nk); clamped to 0..Nk
+ *   doc_q, doc_k [B, Nq], [B, Nk] int32 (both or neither)
+ *   prefix  [B] int32, with causal only, or NULL
+ *   slopes  [Hq] fp32, or NULL (no bias)
+ *   lse     [B, Hq, Nq] fp32, or NULL: natural log of the sum of exp(x_ij)
+ * Keys at or past len_b and keys of a negative document do not count whatever
+ * K and V hold there.  fp32 accumulation and statistics; the probabilities are
+ * rounded to the input type for their product with V.
+ */
+spr_status sparsepr_attend_masked(const spr_masked_params* prm, const void* Q, const void* K,
+                                  const void* V, const int32_t* k_len, const int32_t* doc_q,
+                                  const int32_t* doc_k, const int32_t* prefix,
+                                  const float* slopes, void* O, float* lse, void* ws,
+                                  size_t ws_bytes, int32_t* status, void* stream);
+
+enum { SPR_ACT_NONE = 0, SPR_ACT_GELU = 1, SPR_ACT_GELU_TANH = 2, SPR_ACT_SILU = 3 };
+
+/*
+ * Matrix product with its epilogue, row-major or head-major on either side.
+ * X is [B, Hx, N, dx]: row n of batch b is its Hx slices one after the other,
+ * K = Hx * dx channels (Hx = 1: plain rows).  Y and R are [B, Hy, N, dy] alike,
+ * M = Hy * dy channels.  W is [M, K] row-major.  dx and dy are multiples of 8;
+ * of 64 where Hx (Hy) > 1.  Strides in elements for batch, head, token,
+ * multiples of 8; the last dimension contiguous, rows on 16 bytes.
+ */
+typedef struct {
+  int32_t B, N, Hx, dx, Hy, dy;
+  int64_t x_strides[3], y_strides[3], r_strides[3];
+  int64_t w_stride;  /* elements between rows of W, a multiple of 8 */
+  int32_t dtype;     /* SPR_BF16 or SPR_FP16: every tensor */
+  int32_t act;       /* SPR_ACT_* */
+} spr_project_params;
+
+/* Bytes of workspace a call with these parameters needs (0 on bad params). */
+size_t sparsepr_project_workspace(const spr_project_params* prm);
+
+/*
+ * Y = R + gate_b * act(X W^T + bias): products accumulate in fp32, the epilogue
+ * is fp32, Y is rounded once.  bias [M], gate [B, M] (contiguous) and R (strides
+ * r_strides) may each be NULL.  R may be Y (same strides); any other overlap of
+ * Y with an input is undefined.
+ */
+spr_status sparsepr_project(const spr_project_params* prm, const void* X, const void* W,
+                            const void* bias, const void* gate, const void* R, void* Y, void* ws,
+                            size_t ws_bytes, int32_t* status, void* stream);
+
 /* Library version string (static storage). */
 const char* sparsepr_version(void);
 
