@@ -16,6 +16,7 @@ namespace spr {
 namespace {
 
 constexpr int NR_THREADS = 256;
+constexpr int NR_HEADS = 4;  // heads whose rows a thread has in flight at once
 
 struct NrSide {
   const void* x;
@@ -33,22 +34,28 @@ struct NrArgs {
   int B, d, rot, halves, norm, table_rows, heads_per_group;
 };
 
+// Eight channels as they lie in memory, and as fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f);
-template <>
-__device__ __forceinline__ void load8<bf16>(const bf16* p, float* f) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> fetch8(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+__device__ __forceinline__ void widen(const Raw<bf16>& r, float* f) {
+  const uint32_t u[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = __uint_as_float(u[i] << 16);
     f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float* f) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void widen(const Raw<__half>& r, float* f) {
+  const uint32_t u[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
@@ -56,11 +63,18 @@ __device__ __forceinline__ void load8<__half>(const __half* p, float* f) {
     f[2 * i + 1] = g.y;
   }
 }
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+__device__ __forceinline__ void widen(const Raw<float>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(r.v[i].x);
+    f[4 * i + 1] = __uint_as_float(r.v[i].y);
+    f[4 * i + 2] = __uint_as_float(r.v[i].z);
+    f[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  widen(fetch8(p), f);
 }
 __device__ __forceinline__ void store8(bf16* p, const float* f) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
@@ -83,8 +97,8 @@ __device__ __forceinline__ void store8(float* p, const float* f) {
 // Grid: x tiles of tokens, y groups of heads, z = batch and side.
 template <typename TI, typename TO, int LPR>
 __global__ void __launch_bounds__(NR_THREADS) k_norm_rotate(const __grid_constant__ NrArgs a) {
-  const int b = blockIdx.z >> 1;
-  const NrSide& s = a.side[blockIdx.z & 1];
+  const int b = blockIdx.z % a.B;
+  const NrSide& s = a.side[blockIdx.z / a.B];
   const int h0 = blockIdx.y * a.heads_per_group, h1 = min(s.H, h0 + a.heads_per_group);
   const int l = threadIdx.x % LPR, c0 = 8 * l;  // this lane's channels c0 .. c0 + 7
   const int n = blockIdx.x * (NR_THREADS / LPR) + threadIdx.x / LPR;
@@ -127,49 +141,65 @@ __global__ void __launch_bounds__(NR_THREADS) k_norm_rotate(const __grid_constan
   const int partner = low ? (threadIdx.x & 31) + half / 8 : (threadIdx.x & 31) - half / 8;
   const TI* x = static_cast<const TI*>(s.x) + b * s.xs[0] + (int64_t)n * s.xs[2] + c0;
   TO* y = static_cast<TO*>(s.y) + b * s.ys[0] + (int64_t)n * s.ys[2] + c0;
-  for (int h = h0; h < h1; ++h) {
-    float f[8];
+  for (int hb = h0; hb < h1; hb += NR_HEADS) {
+    Raw<TI> raw[NR_HEADS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    if (live && mine) load8(x + h * s.xs[1], f);
-    if (a.norm) {
-      float q = 0.f;
+    for (int u = 0; u < NR_HEADS; ++u)
+      if (live && mine && hb + u < h1) raw[u] = fetch8(x + (hb + u) * s.xs[1]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(f[i], f[i], q);
+    for (int u = 0; u < NR_HEADS; ++u) {
+      if (hb + u >= h1) break;  // the same for the whole block
+      float f[8];
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-      const float r = rsqrtf(fmaf(q, a.inv_d, a.eps));
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      if (live && mine) widen(raw[u], f);
+      if (a.norm) {
+        float q = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
-    }
-    if (a.rot) {
-      if (a.halves) {
+        for (int i = 0; i < 8; ++i) q = fmaf(f[i], f[i], q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xffffffffu, f[i], partner);
-          if (turned) f[i] = low ? f[i] * cs[i] - o * sn[i] : o * sn[i] + f[i] * cs[i];
-        }
-      } else if (turned) {
+        for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+        const float r = rsqrtf(fmaf(q, a.inv_d, a.eps));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = f[2 * i], q = f[2 * i + 1];
-          f[2 * i] = p * cs[i] - q * sn[i];
-          f[2 * i + 1] = p * sn[i] + q * cs[i];
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+      }
+      if (a.rot) {
+        if (a.halves) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float o = __shfl_sync(0xffffffffu, f[i], partner);
+            if (turned) f[i] = low ? f[i] * cs[i] - o * sn[i] : o * sn[i] + f[i] * cs[i];
+          }
+        } else if (turned) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = f[2 * i], q = f[2 * i + 1];
+            f[2 * i] = p * cs[i] - q * sn[i];
+            f[2 * i + 1] = p * sn[i] + q * cs[i];
+          }
         }
       }
+      if (live && mine) store8(y + (hb + u) * s.ys[1], f);
     }
-    if (live && mine) store8(y + h * s.ys[1], f);
   }
 }
 
 template <typename TI, typename TO>
-cudaError_t launch(const NrArgs& a, cudaStream_t st) {
+cudaError_t launch(NrArgs a, cudaStream_t st) {
   const int lanes = a.d / 8;
   auto go = [&](auto kern, int lpr) {
     const int per = NR_THREADS / lpr;
     const int N = max(a.side[0].N, a.side[1].H ? a.side[1].N : 0);
     const int H = max(a.side[0].H, a.side[1].H);
-    const dim3 grid((N + per - 1) / per, (H + a.heads_per_group - 1) / a.heads_per_group, 2 * a.B);
+    // A thread takes its token's angles and weights once for a group of heads.
+    // Few tokens: one head per thread, so that the row is the only latency.
+    // Many: two rounds of NR_HEADS rows, as soon as that leaves eight blocks
+    // per SM, so that the tables are read an eighth as often as the rows.
+    const int64_t blocks = (int64_t)((N + per - 1) / per) * H * 2 * a.B;
+    const int64_t share = blocks / (8 * num_sms());
+    a.heads_per_group = share >= 2 * NR_HEADS ? 2 * NR_HEADS : share >= NR_HEADS ? NR_HEADS : 1;
+    const dim3 grid((N + per - 1) / per, (H + a.heads_per_group - 1) / a.heads_per_group,
+                    (a.side[1].H ? 2 : 1) * a.B);
     spr_launch(kern, grid, NR_THREADS, 0, st, a);
     return cudaGetLastError();
   };
@@ -253,7 +283,6 @@ extern "C" spr_status sparsepr_norm_rotate(const spr_norm_rotate_params* p, cons
   a.halves = p->pairing == SPR_PAIR_HALVES;
   a.norm = p->norm;
   a.table_rows = table_rows;
-  a.heads_per_group = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (status && cudaMemsetAsync(status, 0, 4 * sizeof(int32_t), st) != cudaSuccess)
     return SPR_ECUDA;

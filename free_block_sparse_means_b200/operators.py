@@ -49,13 +49,30 @@ def _option(name, value, table):
     return table[value]
 
 
-def _same(name, t, struct, shape_fields, stride_field, dtype):
+def _made(prm, **tensors):
+    """Keep with the parameters what the tensors they were made for look like, so that a call with
+    such tensors is checked by three comparisons each."""
+    prm.made_bytes = bytes(prm)
+    prm.made_for = {n: (tuple(t.shape), t.stride(), t.dtype) for n, t in tensors.items()
+                    if t is not None}
+    return prm
+
+
+def _made_for(prm):
+    """What _made kept, as long as no field has been changed since."""
+    kept = prm.__dict__
+    return kept["made_for"] if kept.get("made_bytes") == bytes(prm) else {}
+
+
+def _same(name, t, prm, made, shape_fields, stride_field, dtype):
     """Check that a tensor is the one its parameters were made for."""
+    if isinstance(t, torch.Tensor) and made.get(name) == (t.shape, t.stride(), t.dtype):
+        return
     shape, strides = _dims(name, t)
-    want = tuple(getattr(struct, f) for f in shape_fields)
+    want = tuple(getattr(prm, f) for f in shape_fields)
     if shape != want:
         raise ValueError(f"{name} must have shape {want}, got {shape}")
-    if strides != tuple(getattr(struct, stride_field)):
+    if strides != tuple(getattr(prm, stride_field)):
         raise ValueError(f"{name} must have the strides its parameters were made with")
     if DTYPES.get(t.dtype) != dtype:
         raise ValueError(f"{name} has type {t.dtype}, not the one its parameters were made with")
@@ -64,9 +81,9 @@ def _same(name, t, struct, shape_fields, stride_field, dtype):
 def _aux(name, t, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -76,27 +93,31 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _run(where, tensors, stream, call):
-    """Check the tensors' device and make the call on it."""
-    device = tensors["first"].device
-    if torch.is_grad_enabled():
-        for name, t in tensors.items():
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{where} has no backward pass; {name} requires a gradient "
-                                 "(call it under torch.no_grad())")
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != device):
-            raise ValueError(f"{name} must be on {device}" if device.type == "cuda" else
-                             f"{name} must be on a CUDA device")
+def _run(where, tensors, names, stream, call, *args):
+    """Check where the tensors live (the first one decides) and make the call there."""
+    index = tensors[0].get_device()
+    grad = torch.is_grad_enabled()
+    astray = None
+    for i, t in enumerate(tensors):
+        if t is not None:
+            if grad and t.requires_grad:
+                raise ValueError(f"{where} has no backward pass; {names.split()[i]} requires a "
+                                 "gradient (call it under torch.no_grad())")
+            if t.get_device() != index:
+                astray = i
+    if index < 0 or astray is not None:
+        name = names.split()[astray or 0]
+        raise ValueError(f"{name} must be on {tensors[0].device}" if index >= 0 else
+                         f"{names.split()[0]} must be on a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream must be one of {device}")
-    if device.index == torch.cuda.current_device():
-        _check(where, call(ctypes.c_void_p(stream.cuda_stream)))
+        stream = torch.cuda.current_stream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream must be one of {tensors[0].device}")
+    if index == torch.cuda.current_device():
+        _check(where, call(*args, stream.cuda_stream))
     else:
-        with torch.cuda.device(device):
-            _check(where, call(ctypes.c_void_p(stream.cuda_stream)))
+        with torch.cuda.device(index):
+            _check(where, call(*args, stream.cuda_stream))
 
 
 # ------------------------------------------------------------ norm + rotation
@@ -126,7 +147,7 @@ def make_norm_rotate(Q, K, Qo, Ko, *, eps=1e-6, norm=True, rot=None,
     prm.norm, prm.eps = int(bool(norm)), float(eps)
     prm.rot = d if rot is None else int(rot)
     prm.pairing = _option("pairing", pairing, PAIRINGS)
-    return prm
+    return _made(prm, Q=Q, K=K, Qo=Qo, Ko=Ko)
 
 
 def sparsepr_norm_rotate(prm, Q, K, Qo, Ko, wq=None, wk=None, cos=None, sin=None, pos_q=None,
@@ -137,11 +158,12 @@ def sparsepr_norm_rotate(prm, Q, K, Qo, Ko, wq=None, wk=None, cos=None, sin=None
     pos_q, pos_k: [B, N] int32 table row of each token (None: token n takes row n); status:
     optional int32[4] device tensor.  Qo may be Q and Ko may be K.
     """
-    _same("Q", Q, prm, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype_in)
-    _same("Qo", Qo, prm, ("B", "Hq", "Nq", "d"), "qo_strides", prm.dtype_out)
+    made = _made_for(prm)
+    _same("Q", Q, prm, made, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype_in)
+    _same("Qo", Qo, prm, made, ("B", "Hq", "Nq", "d"), "qo_strides", prm.dtype_out)
     if prm.Hk:
-        _same("K", K, prm, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype_in)
-        _same("Ko", Ko, prm, ("B", "Hk", "Nk", "d"), "ko_strides", prm.dtype_out)
+        _same("K", K, prm, made, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype_in)
+        _same("Ko", Ko, prm, made, ("B", "Hk", "Nk", "d"), "ko_strides", prm.dtype_out)
     elif K is not None or Ko is not None or wk is not None or pos_k is not None:
         raise ValueError("the parameters were made without keys")
     for name, w in (("wq", wq), ("wk", wk)):
@@ -159,12 +181,11 @@ def sparsepr_norm_rotate(prm, Q, K, Qo, Ko, wq=None, wk=None, cos=None, sin=None
             _aux(name, p, torch.int32, (prm.B, n))
     if status is not None:
         _aux("status", status, torch.int32, (4,))
-    _run("sparsepr_norm_rotate",
-         {"first": Q, "K": K, "Qo": Qo, "Ko": Ko, "wq": wq, "wk": wk, "cos": cos, "sin": sin,
-          "pos_q": pos_q, "pos_k": pos_k, "status": status}, stream,
-         lambda st: load_library().sparsepr_norm_rotate(
-             ctypes.byref(prm), Q.data_ptr(), _ptr(K), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin),
-             rows, _ptr(pos_q), _ptr(pos_k), Qo.data_ptr(), _ptr(Ko), _ptr(status), st))
+    _run("sparsepr_norm_rotate", (Q, K, Qo, Ko, wq, wk, cos, sin, pos_q, pos_k, status),
+         "Q K Qo Ko wq wk cos sin pos_q pos_k status", stream,
+         load_library().sparsepr_norm_rotate, ctypes.byref(prm), Q.data_ptr(), _ptr(K), _ptr(wq),
+         _ptr(wk), _ptr(cos), _ptr(sin), rows, _ptr(pos_q), _ptr(pos_k), Qo.data_ptr(), _ptr(Ko),
+         _ptr(status))
 
 
 # ----------------------------------------------------------- masked attention
@@ -191,7 +212,7 @@ def make_masked(Q, K, V, O, *, scale=0.0, softcap=0.0, causal=False,
     prm.scale, prm.softcap = float(scale), float(softcap)
     prm.causal = int(bool(causal))
     prm.q_start = ALIGN_END if q_start is None else int(q_start)
-    return prm
+    return _made(prm, Q=Q, K=K, V=V, O=O)
 
 
 def sparsepr_attend_masked(prm, Q, K, V, O, ws, k_len=None, doc_q=None, doc_k=None, prefix=None,
@@ -203,31 +224,34 @@ def sparsepr_attend_masked(prm, Q, K, V, O, ws, k_len=None, doc_q=None, doc_k=No
     [Hq] fp32; lse: [B, Hq, Nq] fp32 output; status: optional int32[4].  Rows that see no key are
     zero (lse -inf).
     """
-    _same("Q", Q, prm, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype)
-    _same("K", K, prm, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype)
-    _same("V", V, prm, ("B", "Hk", "Nk", "d"), "v_strides", prm.dtype)
-    _same("O", O, prm, ("B", "Hq", "Nq", "d"), "o_strides", prm.dtype)
+    made = _made_for(prm)
+    _same("Q", Q, prm, made, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype)
+    _same("K", K, prm, made, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype)
+    _same("V", V, prm, made, ("B", "Hk", "Nk", "d"), "v_strides", prm.dtype)
+    _same("O", O, prm, made, ("B", "Hq", "Nq", "d"), "o_strides", prm.dtype)
     i32 = torch.int32
-    for name, t, dt, shape in (("k_len", k_len, i32, (prm.B,)), ("prefix", prefix, i32, (prm.B,)),
-                               ("doc_q", doc_q, i32, (prm.B, prm.Nq)),
-                               ("doc_k", doc_k, i32, (prm.B, prm.Nk)),
-                               ("slopes", slopes, torch.float32, (prm.Hq,)),
-                               ("lse", lse, torch.float32, (prm.B, prm.Hq, prm.Nq)),
-                               ("status", status, i32, (4,))):
+    for name, t in (("k_len", k_len), ("prefix", prefix)):
         if t is not None:
-            _aux(name, t, dt, shape)
+            _aux(name, t, i32, (prm.B,))
+    if doc_q is not None:
+        _aux("doc_q", doc_q, i32, (prm.B, prm.Nq))
+    if doc_k is not None:
+        _aux("doc_k", doc_k, i32, (prm.B, prm.Nk))
+    if slopes is not None:
+        _aux("slopes", slopes, torch.float32, (prm.Hq,))
+    if lse is not None:
+        _aux("lse", lse, torch.float32, (prm.B, prm.Hq, prm.Nq))
+    if status is not None:
+        _aux("status", status, i32, (4,))
     if (doc_q is None) != (doc_k is None):
         raise ValueError("doc_q and doc_k go together")
     if prefix is not None and not prm.causal:
         raise ValueError("a prefix needs causal=True")
-    _run("sparsepr_attend_masked",
-         {"first": Q, "K": K, "V": V, "O": O, "ws": ws, "k_len": k_len, "doc_q": doc_q,
-          "doc_k": doc_k, "prefix": prefix, "slopes": slopes, "lse": lse, "status": status},
-         stream,
-         lambda st: load_library().sparsepr_attend_masked(
-             ctypes.byref(prm), Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(k_len),
-             _ptr(doc_q), _ptr(doc_k), _ptr(prefix), _ptr(slopes), O.data_ptr(), _ptr(lse),
-             ws.data_ptr(), ws.numel(), _ptr(status), st))
+    _run("sparsepr_attend_masked", (Q, K, V, k_len, doc_q, doc_k, prefix, slopes, O, lse, ws, status),
+         "Q K V k_len doc_q doc_k prefix slopes O lse ws status", stream,
+         load_library().sparsepr_attend_masked, ctypes.byref(prm), Q.data_ptr(), K.data_ptr(),
+         V.data_ptr(), _ptr(k_len), _ptr(doc_q), _ptr(doc_k), _ptr(prefix), _ptr(slopes),
+         O.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, _ptr(status))
 
 
 # ----------------------------------------------------------------- projection
@@ -254,7 +278,7 @@ def make_project(X, W, Y, *, residual=None, act="none") -> SprProjectParams:
         if t.dtype != X.dtype:
             raise ValueError(f"{name} must be {X.dtype}, got {t.dtype}")
     prm.act = _option("act", act, ACTS)
-    return prm
+    return _made(prm, X=X, W=W, Y=Y, residual=r)
 
 
 def sparsepr_project(prm, X, W, Y, ws, bias=None, gate=None, residual=None, status=None,
@@ -264,22 +288,21 @@ def sparsepr_project(prm, X, W, Y, ws, bias=None, gate=None, residual=None, stat
     bias: [M]; gate: [B, M]; residual: Y's shape (may be Y itself); all of X's type.  status:
     optional int32[4].
     """
-    _same("X", X, prm, ("B", "Hx", "N", "dx"), "x_strides", prm.dtype)
-    _same("Y", Y, prm, ("B", "Hy", "N", "dy"), "y_strides", prm.dtype)
+    made = _made_for(prm)
+    _same("X", X, prm, made, ("B", "Hx", "N", "dx"), "x_strides", prm.dtype)
+    _same("Y", Y, prm, made, ("B", "Hy", "N", "dy"), "y_strides", prm.dtype)
     M, K = prm.Hy * prm.dy, prm.Hx * prm.dx
     if not isinstance(W, torch.Tensor) or W.dtype != X.dtype or tuple(W.shape) != (M, K) or \
             (K > 1 and W.stride(1) != 1) or (M > 1 and W.stride(0) != prm.w_stride):
         raise ValueError("W must be the tensor its parameters were made with")
     if residual is not None:
-        _same("residual", residual, prm, ("B", "Hy", "N", "dy"), "r_strides", prm.dtype)
+        _same("residual", residual, prm, made, ("B", "Hy", "N", "dy"), "r_strides", prm.dtype)
     for name, t, shape in (("bias", bias, (M,)), ("gate", gate, (prm.B, M))):
         if t is not None:
             _aux(name, t, X.dtype, shape)
     if status is not None:
         _aux("status", status, torch.int32, (4,))
-    _run("sparsepr_project",
-         {"first": X, "W": W, "Y": Y, "ws": ws, "bias": bias, "gate": gate,
-          "residual": residual, "status": status}, stream,
-         lambda st: load_library().sparsepr_project(
-             ctypes.byref(prm), X.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(gate),
-             _ptr(residual), Y.data_ptr(), ws.data_ptr(), ws.numel(), _ptr(status), st))
+    _run("sparsepr_project", (X, W, bias, gate, residual, Y, ws, status),
+         "X W bias gate residual Y ws status", stream,
+         load_library().sparsepr_project, ctypes.byref(prm), X.data_ptr(), W.data_ptr(), _ptr(bias),
+         _ptr(gate), _ptr(residual), Y.data_ptr(), ws.data_ptr(), ws.nbytes, _ptr(status))
