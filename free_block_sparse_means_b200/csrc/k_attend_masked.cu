@@ -1,96 +1,842 @@
-// Exact attention under a mask (sparsepr_attend_masked in include/sparsepr.h).
-// One block per (batch, head, 32 queries): keys pass through shared memory 32
-// at a time, each warp keeps 4 query rows with their running maximum, sum and
-// output, each lane one key's score and d / 32 output channels.
+// Exact attention under a mask (sparsepr_attend_masked in include/sparsepr.h) on
+// the 5th-generation tensor cores.
+//
+//   x_ij = cap(scale q_i . k_j) - slope |p_i - j|,  O_i = sum_j softmax_j(x_i) v_j
+//
+// over the keys a query sees.  One pass over the keys with the running maximum
+// m and sum l of every row: S = Q K^T of a 128 x 128 tile lands in TMEM, the
+// softmax warps turn it into P = 2^(x - m) in place, O += P V accumulates in
+// TMEM, and O is rescaled only when a row's maximum grows by more than 2^8 (the
+// final division uses the same stale m, so that is exact).
+//
+// A persistent CTA per SM has two streams of 128 query rows, each with its own
+// S / P and O in TMEM (4 x 128 columns) and its own softmax warpgroup of one
+// row per thread, so that one stream's products run under the other's softmax:
+//   PAIR  the streams are two neighbouring 128-row tiles of a head; a K or V
+//         tile in shared memory serves both.
+//   SOLO  (at most 128 rows share the keys: few query tokens, the heads of a
+//         key head packed into the tile's rows) both streams hold the same
+//         rows and take the key tiles in turn.
+// Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1, warp 8 TMA loads into
+// a ring of K and V tiles, warp 9 issues every product from one thread.  Where
+// the work items do not fill the SMs the keys are split; streams then write
+// (O, m, l) in fp32 and k_am_join adds them up.
+//
+// Masks: with causal and prefix a row sees exactly the keys below one limit,
+// which grows with the row, so a tile is skipped, partly masked or whole by
+// comparing two limits.  Documents are classified per (256 rows, 128 keys) by
+// their id ranges in k_am_documents, which lists the tiles to visit.
+// Keys that count for nobody (past the length, negative document) have their V
+// rows zeroed in shared memory before the product: 0 x NaN would be NaN.
+//
+// Every mbarrier wait is bounded, as in the routed attention kernel.
 #include <cuda_fp16.h>
 
-#include "spr_internal.cuh"
+#include "tc_sm100.cuh"
 
 namespace spr {
 namespace {
 
+constexpr int TBM = 128, TBN = 128;  // query rows of a stream, keys of a tile
+constexpr uint32_t BOX = TBN * 128;  // one swizzled box of 128 rows x 64 channels: 16 KB
+constexpr int AM_THREADS = 384;      // two softmax warpgroups; a loading, an issuing and two idle warps
+// Registers: 168 a thread at launch (64,512 in all); a softmax thread holds a row of 128 scores.
+// 2 x 128 x 208 + 128 x 88 = 64,512.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S0 | S1 | O0 | O1, 128 columns each
+constexpr uint64_t WAIT_NS = 2000000000ull;  // 2 s
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
+
+template <int D>
+__host__ __device__ constexpr uint32_t tile_bytes() { return TBN * D * 2; }
+template <int D>
+__host__ __device__ constexpr int ring() { return D == 128 ? 5 : 8; }  // K and V tiles in flight
+template <int D>
+__host__ __device__ constexpr size_t smem_bytes() {
+  return 1024 + (2 + ring<D>()) * (size_t)tile_bytes<D>() + 512;
+}
+
 struct AmArgs {
-  const void *Q, *K, *V;
   void* O;
   float* lse;
   const int32_t *k_len, *doc_q, *doc_k, *prefix;
   const float* slopes;
-  int64_t qs[3], ks[3], vs[3], os[3];
+  int64_t os[3];
   int B, Hq, Hk, Nq, Nk, causal, q_start;
+  int qmul_b, qmul_h, kmul_b, kmul_h, vmul_b, vmul_h;  // 0 where a TMA dimension has one entry
   float scale, softcap;
+  // the plan: tiles of rows (heads packed per tile `pack`, query blocks `nqb`), key splits
+  int pack, ntile_h, nqb, nsplit, n_items, partial;
+  // workspace: per row tile its listed key tiles (documents), partial results
+  const int32_t *doc_count, *doc_list;
+  int ktiles;
+  float *part_o, *part_ml;
+  int part_rows;  // rows of a row tile that partial results hold
+  int32_t* status;
 };
 
-__device__ __forceinline__ float tof(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float tof(__half v) { return __half2float(v); }
-__device__ __forceinline__ void put(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256) k_attend_simple(const __grid_constant__ AmArgs a) {
-  __shared__ float sk[32][D + 1];
-  __shared__ T sv[32][D];
-  __shared__ float sq[32][D];
-  const int b = blockIdx.z, h = blockIdx.y, i0 = blockIdx.x * 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = h / (a.Hq / a.Hk);
-  const T* Q = static_cast<const T*>(a.Q) + b * a.qs[0] + h * a.qs[1];
-  const T* K = static_cast<const T*>(a.K) + b * a.ks[0] + hk * a.ks[1];
-  const T* V = static_cast<const T*>(a.V) + b * a.vs[0] + hk * a.vs[1];
-  const int len = a.k_len ? min(max(a.k_len[b], 0), a.Nk) : a.Nk;
-  const int pos0 = a.q_start == SPR_ALIGN_END ? len - a.Nq : a.q_start;
-  const int pre = a.prefix ? a.prefix[b] : 0;
-  for (int i = threadIdx.x; i < 32 * D; i += 256)
-    sq[i / D][i % D] = i0 + i / D < a.Nq ? tof(Q[(int64_t)(i0 + i / D) * a.qs[2] + i % D]) : 0.f;
-  float m[4], l[4], o[4][D / 32];
-  for (int r = 0; r < 4; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-    for (int c = 0; c < D / 32; ++c) o[r][c] = 0.f;
+// What the mask leaves of one batch's keys for query rows first .. last: rows see
+// the keys below limit(row), which does not decrease with the row.
+struct Limits {
+  int len, pre, pos0, causal;
+  __device__ __forceinline__ void init(const AmArgs& a, int b) {
+    len = a.k_len ? min(max(a.k_len[b], 0), a.Nk) : a.Nk;
+    pre = a.prefix ? min(max(a.prefix[b], 0), len) : 0;
+    pos0 = a.q_start == SPR_ALIGN_END ? len - a.Nq : a.q_start;
+    causal = a.causal;
   }
-  for (int j0 = 0; j0 < len; j0 += 32) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * D; i += 256) {
-      const int j = j0 + i / D;
-      const bool dead = j >= len || (a.doc_k && a.doc_k[(int64_t)b * a.Nk + j] < 0);
-      sk[i / D][i % D] = dead ? 0.f : tof(K[(int64_t)j * a.ks[2] + i % D]);
-      sv[i / D][i % D] = dead ? T(0.f) : V[(int64_t)j * a.vs[2] + i % D];
+  __device__ __forceinline__ int limit(int row) const {
+    return causal ? max(min(pos0 + row + 1, len), pre) : len;
+  }
+};
+
+// One work item: a row tile (or pair of them) and its share of the key tiles.
+template <bool SOLO>
+struct Item {
+  int b, h0, q0, tile;       // batch, first query head, first query row, row tile (b, h, block)
+  int nt0, nt1;              // key tiles each stream visits
+  int i0, n;                 // first entry and entries of this item's list
+  const int32_t* list;       // documents: the listed tiles
+  Limits lim;
+  __device__ void init(const AmArgs& a, int item) {
+    const int split = item % a.nsplit;
+    tile = item / a.nsplit;
+    const int blk = tile % a.nqb;
+    int t = tile / a.nqb;
+    const int ht = t % a.ntile_h;
+    b = t / a.ntile_h;
+    // heads: `pack` query heads per tile within a key head
+    const int rep = a.Hq / a.Hk, per = (rep + a.pack - 1) / a.pack;
+    h0 = (ht / per) * rep + (ht % per) * a.pack;
+    // blocks with the most keys first: later items then even out the SMs
+    q0 = (a.causal ? a.nqb - 1 - blk : blk) * (SOLO ? TBM : 2 * TBM);
+    lim.init(a, b);
+    nt0 = tiles(a, 0);
+    nt1 = SOLO ? nt0 : tiles(a, 1);
+    int most = max(nt0, nt1);
+    list = nullptr;
+    if (a.doc_q) {
+      const int64_t at = (int64_t)b * a.nqb + q0 / (SOLO ? TBM : 2 * TBM);
+      list = a.doc_list + at * a.ktiles;
+      most = a.doc_count[at];
     }
-    __syncthreads();
-    const int j = j0 + lane;
-    const int dk = a.doc_k && j < len ? a.doc_k[(int64_t)b * a.Nk + j] : 0;
-    for (int r = 0; r < 4; ++r) {
-      const int i = i0 + 4 * warp + r;
-      float x = 0.f;
-      for (int c = 0; c < D; ++c) x = fmaf(sq[4 * warp + r][c], sk[lane][c], x);
-      x *= a.scale;
-      if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-      const int p = pos0 + i;
-      if (a.slopes) x -= a.slopes[h] * fabsf((float)(p - j));
-      bool see = i < a.Nq && j < len;
-      if (a.doc_k) see = see && dk >= 0 && a.doc_q[(int64_t)b * a.Nq + min(i, a.Nq - 1)] == dk;
-      if (a.causal) see = see && (j <= p || j < pre);
-      if (!see) x = -INFINITY;
-      const float mn = fmaxf(m[r], warp_max(x));
-      const float ms = mn == -INFINITY ? 0.f : mn;
-      const float e = expf(x - ms), corr = expf(m[r] - ms);
-      l[r] = l[r] * corr + warp_sum(e);
-      m[r] = mn;
-      for (int c = 0; c < D / 32; ++c) o[r][c] *= corr;
-      for (int k = 0; k < 32; ++k) {
-        const float w = __shfl_sync(0xffffffffu, e, k);
-        for (int c = 0; c < D / 32; ++c) o[r][c] = fmaf(w, tof(sv[k][lane + 32 * c]), o[r][c]);
+    const int share = (most + a.nsplit - 1) / a.nsplit;
+    i0 = min(most, split * share);
+    n = min(most, i0 + share) - i0;
+  }
+  __device__ __forceinline__ int tiles(const AmArgs& a, int s) const {
+    const int first = q0 + s * TBM, last = min(first + TBM, a.Nq) - 1;
+    return first < a.Nq ? (lim.limit(last) + TBN - 1) / TBN : 0;
+  }
+  // entry i: key tile and bits (1, 2: stream 0, 1 visits it; 4, 8: whole for it by documents;
+  // 16: holds keys that count for nobody)
+  __device__ __forceinline__ int entry(int i, int& bits) const {
+    if (list) {
+      const int e = list[i0 + i];
+      bits = e & 31;
+      return e >> 5;
+    }
+    const int t = i0 + i;
+    bits = 12 | (t < nt0 ? 1 : 0) | (t < nt1 ? 2 : 0) | ((t + 1) * TBN > lim.len ? 16 : 0);
+    return t;
+  }
+  __device__ __forceinline__ bool visits(int i, int s) const {
+    if (SOLO) return (i & 1) == s;
+    int bits;
+    entry(i, bits);
+    return bits >> s & 1;
+  }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n.reg .b64 ra, rb, rc, rd;\n"
+      "mov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\nmov.b64 rc, {%5, %5};\n"
+      "fma.rn.ftz.f32x2 rd, ra, rb, rc;\nmov.b64 {%0, %1}, rd;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n.reg .b64 ra, rd;\n"
+      "mov.b64 ra, {%2, %3};\nmov.b64 rd, {%0, %1};\n"
+      "add.rn.ftz.f32x2 rd, rd, ra;\nmov.b64 {%0, %1}, rd;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<bf16>(float lo, float hi) { return pack_bf16(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// fp16 probabilities are scaled by 2^7: with the stale maximum they reach 2^15,
+// and values down to 2^-21 of the row's largest stay normal numbers.
+template <typename T>
+constexpr float p_shift() { return sizeof(T) == 2 && std::is_same<T, __half>::value ? 7.f : 0.f; }
+
+// XF: scores are capped or get the distance bias (both optional at run time).
+template <typename T, int D, bool SOLO, bool XF>
+__global__ void __launch_bounds__(AM_THREADS, 1)
+    k_attend_masked(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AmArgs a) {
+  constexpr uint32_t TILE = tile_bytes<D>();
+  constexpr int NST = ring<D>(), NBOX = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = base;             // two tiles (SOLO: the first)
+  uint8_t* sKV = base + 2 * TILE;  // ring: K and V tiles in turn
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + (2 + NST) * TILE);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* s_full = bars + 2;   // [2]
+  uint64_t* p_full = bars + 4;   // [2]
+  uint64_t* o_full = bars + 6;   // [2]
+  uint64_t* o_free = bars + 8;   // [2]
+  uint64_t* drain = bars + 10;
+  uint64_t* full = bars + 11;          // [NST]
+  uint64_t* empty = bars + 11 + NST;   // [NST]
+  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(bars + 11 + 2 * NST);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_base_s + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(q_full, 1);
+    tc::mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(s_full + s, 1);
+      tc::mbar_init(p_full + s, TBM);
+      tc::mbar_init(o_full + s, 1);
+      tc::mbar_init(o_free + s, TBM);
+    }
+    tc::mbar_init(drain, 1);
+    for (int s = 0; s < NST; ++s) {
+      tc::mbar_init(full + s, 1);
+      tc::mbar_init(empty + s, 1);
+    }
+    *abort_s = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(tmem_base_s, TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tbase = *tmem_base_s;
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(OTHER_REGS));
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      tc::prefetch_tmap(&tmQ);
+      tc::prefetch_tmap(&tmK);
+      tc::prefetch_tmap(&tmV);
+      int c = 0, items = 0;  // tiles loaded into the ring, items with work
+      bool ok = true;
+      const uint32_t qbox = a.pack > 1 ? (uint32_t)(a.pack * a.Nq) * 128u : BOX;
+      const int rep = a.Hq / a.Hk;
+      for (int w = blockIdx.x; w < a.n_items && ok; w += gridDim.x) {
+        Item<SOLO> it;
+        it.init(a, w);
+        if (it.n == 0) continue;
+        auto load_kv = [&](const CUtensorMap* m, int t, int mb, int mh) {
+          const int s = c % NST;
+          if (c >= NST && !tc::mbar_wait(empty + s, ((c / NST) - 1) & 1, abort_s, WAIT_NS))
+            return false;
+          tc::mbar_expect_tx(full + s, TILE);
+          for (int j = 0; j < NBOX; ++j)
+            tc::tma_load_4d(sKV + (size_t)s * TILE + j * BOX, m, 64 * j, t * TBN,
+                            (it.h0 / rep) * mh, it.b * mb, full + s);
+          ++c;
+          return true;
+        };
+        int bits;
+        int t = it.entry(0, bits);
+        if (!(ok = load_kv(&tmK, t, a.kmul_b, a.kmul_h))) break;
+        if (items > 0 && !tc::mbar_wait(q_empty, (items - 1) & 1, abort_s, WAIT_NS)) break;
+        const int nq = SOLO ? 1 : 2;
+        tc::mbar_expect_tx(q_full, nq * NBOX * qbox);
+        for (int s = 0; s < nq; ++s)
+          for (int j = 0; j < NBOX; ++j)
+            tc::tma_load_4d(sQ + s * TILE + j * BOX, &tmQ, 64 * j, it.q0 + s * TBM,
+                            it.h0 * a.qmul_h, it.b * a.qmul_b, q_full);
+        ++items;
+        for (int i = 0; i < it.n && ok; ++i) {
+          if (i > 0) {
+            t = it.entry(i, bits);
+            if (!(ok = load_kv(&tmK, t, a.kmul_b, a.kmul_h))) break;
+          }
+          ok = load_kv(&tmV, t, a.vmul_b, a.vmul_h);
+        }
+      }
+      if (*abort_s) {  // let our copies in flight land before the block exits
+        for (int k = c - NST; k < c; ++k)
+          if (k >= 0) tc::mbar_wait_bounded(full + (k % NST), (k / NST) & 1, 100000000ull);
+        if (items > 0) tc::mbar_wait_bounded(q_full, (items - 1) & 1, 100000000ull);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr bool BF = std::is_same<T, bf16>::value;
+      constexpr uint32_t idS = BF ? tc::idesc_bf16(TBM, TBN, 0) : tc::idesc_fp16(TBM, TBN, 0);
+      constexpr uint32_t idPV = BF ? tc::idesc_bf16(TBM, D, 1) : tc::idesc_fp16(TBM, D, 1);
+      const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t kd = tc::smem_desc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t vd = tc::smem_desc_sw128(smem_u32(sKV), BOX, 1024);
+      int c = 0;                     // ring entries of the items before this one
+      int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, items finished, per stream
+      int items = 0;
+      auto wait_ring = [&](int k) {
+        return tc::mbar_wait(full + k % NST, (k / NST) & 1, abort_s, WAIT_NS);
+      };
+      auto issue_s = [&](int s, int k) {
+        tc::tc_fence_after();
+        const uint64_t q = qd + (SOLO ? 0 : (uint64_t)(s * (TILE >> 4)));
+        const uint64_t b = kd + (uint64_t)((k % NST) * (TILE >> 4));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * BOX + (ks & 3) * 32) >> 4;
+          tc::mma_ss(tbase + s * 128, q + off, b + off, idS, ks > 0);
+        }
+        tc::mma_commit(s_full + s);
+      };
+      auto issue_pv = [&](int s, int k, bool first) {
+        tc::tc_fence_after();
+        const uint64_t b = vd + (uint64_t)((k % NST) * (TILE >> 4));
+#pragma unroll
+        for (int kk = 0; kk < TBN / 16; ++kk)
+          tc::mma_ts(tbase + O_COL + s * 128, tbase + s * 128 + kk * 8, b + kk * (2048 >> 4), idPV,
+                     !(first && kk == 0));
+      };
+      bool ok = true;
+      for (int w = blockIdx.x; w < a.n_items && ok; w += gridDim.x) {
+        Item<SOLO> it;
+        it.init(a, w);
+        if (it.n == 0) continue;
+        if (!(ok = tc::mbar_wait(q_full, items & 1, abort_s, WAIT_NS))) break;
+        bool first[2] = {true, true};
+        // the first tile's scores (SOLO: of both streams' first tiles)
+        if (!(ok = wait_ring(c))) break;
+        if (SOLO || it.visits(0, 0)) issue_s(0, c);
+        if (!SOLO && it.visits(0, 1)) issue_s(1, c);
+        tc::mma_commit(empty + c % NST);
+        if (SOLO && it.n > 1) {
+          if (!(ok = wait_ring(c + 2))) break;
+          issue_s(1, c + 2);
+          tc::mma_commit(empty + (c + 2) % NST);
+        }
+        constexpr int AHEAD = SOLO ? 2 : 1;  // tiles between a stream's product and its next scores
+        if (it.n <= AHEAD) tc::mma_commit(q_empty);
+        for (int i = 0; i < it.n && ok; ++i) {
+          const int kv = c + 2 * i + 1, kn = c + 2 * (i + AHEAD);
+          const bool more = i + AHEAD < it.n;
+          if (!(ok = wait_ring(kv))) break;
+          bool have_k = false;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok) break;
+            if (it.visits(i, s)) {
+              if (!(ok = tc::mbar_wait(p_full + s, np[s] & 1, abort_s, WAIT_NS))) break;
+              ++np[s];
+              if (first[s] && no[s] > 0 &&
+                  !(ok = tc::mbar_wait(o_free + s, (no[s] - 1) & 1, abort_s, WAIT_NS)))
+                break;
+              issue_pv(s, kv, first[s]);
+              first[s] = false;
+            }
+            if (more && it.visits(i + AHEAD, s)) {
+              if (!have_k && !(ok = wait_ring(kn))) break;
+              have_k = true;
+              issue_s(s, kn);
+            }
+          }
+          if (!ok) break;
+          tc::mma_commit(empty + kv % NST);
+          if (more) {
+            if (!have_k && !(ok = wait_ring(kn))) break;
+            tc::mma_commit(empty + kn % NST);
+            if (i + AHEAD + 1 == it.n) tc::mma_commit(q_empty);
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (!first[s]) {
+            tc::mma_commit(o_full + s);
+            ++no[s];
+          }
+        c += 2 * it.n;
+        ++items;
+      }
+      tc::mma_commit(drain);
+      tc::mbar_wait_bounded(drain, 0, WAIT_NS);
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(SOFTMAX_REGS));
+    const int s = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_f = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t scol = tbase + lane_f + s * 128, ocol = tbase + lane_f + O_COL + s * 128;
+    const float scale_log2 = a.scale * LOG2E;
+    int np = 0, no = 0, c = 0;  // tiles and items this stream has had, ring entries so far
+    bool ok = true;
+    for (int w = blockIdx.x; w < a.n_items && ok; w += gridDim.x) {
+      Item<SOLO> it;
+      it.init(a, w);
+      // this thread's row: query head and query
+      int h = it.h0, qi = it.q0 + (SOLO ? 0 : s * TBM) + row;
+      bool live = qi < a.Nq;
+      if (a.pack > 1) {
+        const int g = row / a.Nq, rep = a.Hq / a.Hk;
+        qi = row - g * a.Nq;
+        h = it.h0 + g;
+        live = g < a.pack && h < (it.h0 / rep + 1) * rep;
+        if (!live) qi = 0, h = it.h0;
+      }
+      const int whole = it.lim.limit(it.q0 + (SOLO ? 0 : s * TBM));  // keys every row of the tile sees
+      const int lim = live ? it.lim.limit(qi) : 0;
+      const int docq = a.doc_q && live ? a.doc_q[(int64_t)it.b * a.Nq + qi] : 0;
+      const float slope = XF && a.slopes ? a.slopes[h] * LOG2E : 0.f;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int i = 0; i < it.n; ++i) {
+        int bits;
+        const int t = it.entry(i, bits);
+        if (SOLO ? (i & 1) != s : !(bits >> s & 1)) continue;
+        const bool got_s = tc::mbar_wait(s_full + s, np & 1, abort_s, WAIT_NS);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, got_s)) {
+          ok = false;
+          break;
+        }
+        ++np;
+        tc::tc_fence_after();
+        uint32_t sr[TBN];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::tmem_ld32(scol + 32 * k, sr + 32 * k);
+        tc::tmem_wait_ld();
+        const int t0 = t * TBN;
+        float sl2 = scale_log2;
+        if (XF) {
+          if (a.softcap > 0.f) {  // c tanh(z) = c - 2 c / (1 + e^(2 z)), in units of log 2
+            const float zin = 2.f * scale_log2 / a.softcap, cl = a.softcap * LOG2E;
+#pragma unroll
+            for (int k = 0; k < TBN; ++k)
+              sr[k] = __float_as_uint(
+                  fmaf(-2.f * cl, rcp(1.f + ex2(__uint_as_float(sr[k]) * zin)), cl));
+          } else {
+#pragma unroll
+            for (int k = 0; k < TBN; ++k)
+              sr[k] = __float_as_uint(__uint_as_float(sr[k]) * scale_log2);
+          }
+          if (a.slopes) {
+            const float at = (float)(it.lim.pos0 + qi - t0);
+#pragma unroll
+            for (int k = 0; k < TBN; ++k)
+              sr[k] = __float_as_uint(
+                  fmaf(-slope, fabsf(at - (float)k), __uint_as_float(sr[k])));
+          }
+          sl2 = 1.f;
+        }
+        if (!(bits >> (SOLO ? 2 : 2 + s) & 1) || t0 + TBN > whole) {
+          const int left = lim - t0;
+#pragma unroll
+          for (int k = 0; k < TBN; ++k)
+            if (k >= left) sr[k] = __float_as_uint(-INFINITY);
+          if (a.doc_k && !(bits >> (SOLO ? 2 : 2 + s) & 1)) {
+            const int32_t* dk = a.doc_k + (int64_t)it.b * a.Nk;
+#pragma unroll
+            for (int k = 0; k < TBN; ++k) {
+              const int id = __ldg(dk + min(t0 + k, a.Nk - 1));
+              if (id != docq || id < 0) sr[k] = __float_as_uint(-INFINITY);
+            }
+          }
+        }
+        float mx8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          mx8[e] = fmaxf(__uint_as_float(sr[e]), __uint_as_float(sr[e + 8]));
+#pragma unroll
+        for (int k = 16; k < TBN; k += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            mx8[e] = max3(mx8[e], __uint_as_float(sr[k + e]), __uint_as_float(sr[k + 8 + e]));
+        const float mx = fmaxf(max3(mx8[0], mx8[1], mx8[2]),
+                               max3(max3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])) * sl2;
+        const float mn = fmaxf(m, mx);
+        float m_use = m;
+        bool rescale = false;
+        if (mn > m + 8.f) {
+          m_use = mn;
+          rescale = !first;
+        }
+        const float corr = rescale ? ex2(m - m_use) : 1.f;
+        // a row that has seen nothing keeps m = -inf; its probabilities are 2^-inf = 0
+        const float neg = m_use == -INFINITY ? 0.f : p_shift<T>() - m_use;
+        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t pr[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            fma2(x0, x1, __uint_as_float(sr[32 * k + 2 * e]), __uint_as_float(sr[32 * k + 2 * e + 1]),
+                 sl2, neg);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            add2(sum4[2 * (e & 1)], sum4[2 * (e & 1) + 1], p0, p1);
+            pr[e] = pack2<T>(p0, p1);
+          }
+          __syncwarp();
+          tc::tmem_st16(scol + 16 * k, pr);
+        }
+        if (__any_sync(0xffffffffu, rescale)) {  // the products before S(i) are done: O is at rest
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            __syncwarp();
+            tc::tmem_ld32(ocol + 32 * k, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            __syncwarp();
+            tc::tmem_st32(ocol + 32 * k, o);
+          }
+        }
+        l = l * corr + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+        m = m_use;
+        first = false;
+        if (bits & 16) {  // zero the V rows of keys that count for nobody
+          const int kv = c + 2 * i + 1;
+          const bool got_v = tc::mbar_wait(full + kv % NST, (kv / NST) & 1, abort_s, WAIT_NS);
+          const int j = t0 + row;
+          const bool dead = j >= it.lim.len ||
+                            (a.doc_k && a.doc_k[(int64_t)it.b * a.Nk + j] < 0);
+          if (got_v && dead) {
+            uint8_t* v = sKV + (size_t)(kv % NST) * TILE + row * 128;
+#pragma unroll
+            for (int k = 0; k < NBOX; ++k)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(v + k * BOX + 16 * e) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, got_v)) {
+            ok = false;
+            break;
+          }
+        }
+        __syncwarp();
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(p_full + s);
+      }
+      if (!ok) break;
+      c += 2 * it.n;
+      const bool any = !first;
+      if (any) {
+        const bool got_o = tc::mbar_wait(o_full + s, no & 1, abort_s, WAIT_NS);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, got_o)) {
+          ok = false;
+          break;
+        }
+        ++no;
+        tc::tc_fence_after();
+      }
+      if (a.partial) {
+        const int64_t part = ((int64_t)w * 2 + s) * a.part_rows + row;
+        if (live) {
+          a.part_ml[2 * part] = m;
+          a.part_ml[2 * part + 1] = l;
+        }
+        if (any)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            __syncwarp();
+            tc::tmem_ld32(ocol + 32 * k, o);
+            tc::tmem_wait_ld();
+            if (live) {
+              uint4* d = reinterpret_cast<uint4*>(a.part_o + part * D + 32 * k);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                d[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+      } else {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // NaN sums stay NaN
+        const float f = l == l ? inv : l;
+        uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.O) + it.b * a.os[0] + h * a.os[1] +
+                                            (int64_t)qi * a.os[2]);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[32];
+          if (any) {
+            __syncwarp();
+            tc::tmem_ld32(ocol + 32 * k, o);
+            tc::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                u[g] = l == 0.f ? 0u
+                                : pack2<T>(__uint_as_float(o[8 * e + 2 * g]) * f,
+                                           __uint_as_float(o[8 * e + 2 * g + 1]) * f);
+              d[4 * k + e] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+        }
+        if (live && a.lse)
+          a.lse[((int64_t)it.b * a.Hq + h) * a.Nq + qi] =
+              l == 0.f ? -INFINITY : (m - p_shift<T>()) * LN2 + logf(l);
+      }
+      if (any) {
+        tc::tc_fence_before();
+        tc::mbar_arrive(o_free + s);
       }
     }
   }
-  for (int r = 0; r < 4; ++r) {
-    const int i = i0 + 4 * warp + r;
-    if (i >= a.Nq) break;
-    T* O = static_cast<T*>(a.O) + b * a.os[0] + h * a.os[1] + (int64_t)i * a.os[2];
-    const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-    for (int c = 0; c < D / 32; ++c) put(O + lane + 32 * c, o[r][c] * inv);
-    if (a.lse && lane == 0)
-      a.lse[((int64_t)b * a.Hq + h) * a.Nq + i] = l[r] > 0.f ? m[r] + logf(l[r]) : -INFINITY;
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (threadIdx.x == 0 && *abort_s && a.status && atomicCAS(a.status, 0, (int)ERR_TIMEOUT) == 0)
+    a.status[1] = blockIdx.x;
+  if (warp == 9) {
+    __syncwarp();
+    tc::tmem_dealloc(tbase, TMEM_COLS);
   }
+}
+
+// Add up the partial results of a row: a warp per row, parts = 2 nsplit.
+template <typename T, int D, bool SOLO>
+__global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs a) {
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // (batch, head, query)
+  const int lane = threadIdx.x & 31;
+  if (r >= (int64_t)a.B * a.Hq * a.Nq) return;
+  const int qi = (int)(r % a.Nq), h = (int)(r / a.Nq % a.Hq), b = (int)(r / a.Nq / a.Hq);
+  const int rep = a.Hq / a.Hk, per = (rep + a.pack - 1) / a.pack;
+  const int ht = h / rep * per + h % rep / a.pack;
+  const int span = SOLO ? TBM : 2 * TBM;
+  const int blk = a.causal ? a.nqb - 1 - qi / span : qi / span;
+  const int64_t tile = ((int64_t)b * a.ntile_h + ht) * a.nqb + blk;
+  const int s = SOLO ? 0 : qi % span / TBM;
+  const int row = a.pack > 1 ? h % rep % a.pack * a.Nq + qi : qi % TBM;
+  const int np = SOLO ? 2 * a.nsplit : a.nsplit, step = SOLO ? 1 : 2;
+  const int64_t p0 = (tile * a.nsplit * 2 + s) * a.part_rows + row;
+  const int64_t pstep = (int64_t)step * a.part_rows;
+  float M = -INFINITY;
+  for (int p = lane; p < np; p += 32) M = fmaxf(M, a.part_ml[2 * (p0 + p * pstep)]);
+  M = warp_max(M);
+  constexpr int E = D / 32;
+  float o[E] = {}, l = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < np; ++p) {
+    const int64_t at = p0 + p * pstep;
+    const float m = a.part_ml[2 * at], lp = a.part_ml[2 * at + 1];
+    if (lp == 0.f) continue;  // saw nothing; its O is not written
+    const float w = ex2(m - M);
+    l += w * lp;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(w, a.part_o[at * D + E * lane + e], o[e]);
+  }
+  const float f = l != 0.f ? 1.f / l : 0.f;
+  T* O = static_cast<T*>(a.O) + b * a.os[0] + h * a.os[1] + (int64_t)qi * a.os[2] + E * lane;
+  const uint32_t u0 = pack2<T>(o[0] * f, o[1] * f);
+  if (E == 4) {
+    *reinterpret_cast<uint2*>(O) = make_uint2(u0, pack2<T>(o[E - 2] * f, o[E - 1] * f));
+  } else {
+    *reinterpret_cast<uint32_t*>(O) = u0;
+  }
+  if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -INFINITY : (M - p_shift<T>()) * LN2 + logf(l);
+}
+
+// The key tiles that a row tile has to visit under documents: a block per (row
+// tile, batch), a warp per key tile, 32 tiles at a time.  A tile whose ids do
+// not meet the rows' range is left out; it is whole for a stream when rows and
+// keys all carry one id.
+template <bool SOLO>
+__global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ AmArgs a,
+                                                       int32_t* count, int32_t* list) {
+  __shared__ int lo[2], hi[2], neg[2], entry[32];
+  const int b = blockIdx.y, blk = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int span = SOLO ? TBM : 2 * TBM, q0 = blk * span;
+  if (threadIdx.x < 2) {
+    lo[threadIdx.x] = INT32_MAX;
+    hi[threadIdx.x] = -1;
+    neg[threadIdx.x] = 0;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < span && q0 + (int)threadIdx.x < a.Nq) {
+    const int id = a.doc_q[(int64_t)b * a.Nq + q0 + threadIdx.x], s = threadIdx.x / TBM;
+    if (id >= 0) {
+      atomicMin(&lo[s], id);
+      atomicMax(&hi[s], id);
+    } else {
+      neg[s] = 1;
+    }
+  }
+  __syncthreads();
+  Limits lim;
+  lim.init(a, b);
+  int nt[2];
+  for (int s = 0; s < 2; ++s) {
+    const int first = SOLO ? q0 : q0 + s * TBM, last = min(first + TBM, a.Nq) - 1;
+    nt[s] = first < a.Nq ? (lim.limit(last) + TBN - 1) / TBN : 0;
+  }
+  const int64_t at = (int64_t)b * a.nqb + blk;
+  int32_t* out = list + at * a.ktiles;
+  int n = 0;
+  const int most = max(nt[0], nt[1]);
+  for (int tb = 0; tb < most; tb += 32) {
+    const int t = tb + warp;
+    int bits = 0;
+    if (t < most) {
+      int kl = INT32_MAX, kh = -1;
+      bool dead = (t + 1) * TBN > lim.len;
+      for (int k = 0; k < 4; ++k) {
+        const int j = t * TBN + 32 * k + lane;
+        const int id = j < lim.len ? a.doc_k[(int64_t)b * a.Nk + j] : -1;
+        if (id >= 0) {
+          kl = min(kl, id);
+          kh = max(kh, id);
+        } else {
+          dead = true;
+        }
+      }
+      kl = __reduce_min_sync(0xffffffffu, kl);
+      kh = __reduce_max_sync(0xffffffffu, kh);
+      dead = __any_sync(0xffffffffu, dead);
+      for (int s = 0; s < 2; ++s) {
+        const int r = SOLO ? 0 : s;
+        if (t < nt[r] && kl <= hi[r] && lo[r] <= kh) {
+          bits |= 1 << s;
+          if (kl == kh && lo[r] == hi[r] && !neg[r] && !dead) bits |= 4 << s;
+        }
+      }
+      if (dead) bits |= 16;
+    }
+    if (lane == 0) entry[warp] = bits & 3 ? t << 5 | bits : -1;
+    __syncthreads();
+    if (warp == 0) {
+      const int e = entry[lane];
+      const uint32_t keep = __ballot_sync(0xffffffffu, e >= 0);
+      if (e >= 0) out[n + __popc(keep & ((1u << lane) - 1))] = e;
+      n += __popc(keep);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) count[at] = n;
+}
+
+// The plan of a call: which form, how many items, what the workspace holds.
+struct Plan {
+  bool solo;
+  int pack, ntile_h, nqb, nsplit, n_items, ktiles, part_rows;
+  size_t count_off, list_off, o_off, ml_off, total;
+};
+
+Plan make_plan(const spr_masked_params& p, int sms) {
+  Plan q{};
+  const int rep = p.Hq / p.Hk;
+  // Up to 128 rows that share their keys form one tile: the query tokens of a
+  // head, or of as many heads of the key head as fit.
+  q.solo = p.Nq <= TBM;
+  q.pack = q.solo && 2 * p.Nq <= TBM ? (rep < TBM / p.Nq ? rep : TBM / p.Nq) : 1;
+  q.ntile_h = p.Hk * ((rep + q.pack - 1) / q.pack);
+  q.nqb = q.solo ? 1 : (p.Nq + 2 * TBM - 1) / (2 * TBM);
+  q.ktiles = (p.Nk + TBN - 1) / TBN;
+  const int64_t tiles = (int64_t)p.B * q.ntile_h * q.nqb;
+  q.nsplit = 1;
+  if (tiles < sms) {
+    const int most = (q.ktiles + 3) / 4;  // four key tiles a split at least
+    q.nsplit = (int)(sms / tiles) < most ? (int)(sms / tiles) : most;
+    if (q.nsplit < 1) q.nsplit = 1;
+  }
+  q.n_items = (int)(tiles * q.nsplit);
+  q.part_rows = q.solo ? q.pack * p.Nq : TBM;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t off = at;
+    at += (bytes + 255) / 256 * 256;
+    return off;
+  };
+  q.count_off = take((size_t)p.B * q.nqb * 4);
+  q.list_off = take((size_t)p.B * q.nqb * q.ktiles * 4);
+  const bool partial = q.solo || q.nsplit > 1;
+  q.o_off = take(partial ? (size_t)q.n_items * 2 * q.part_rows * p.d * 4 : 0);
+  q.ml_off = take(partial ? (size_t)q.n_items * 2 * q.part_rows * 8 : 0);
+  q.total = at;
+  return q;
+}
+
+// [B, H, N, d] as a TMA map of boxes of `rows` x `heads` rows of 64 channels.
+// A dimension of stride 0 becomes one entry whose coordinate stays 0.
+bool make_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int B, int H, int N, int d,
+              const int64_t* s, int rows, int heads, int* mul_b, int* mul_h) {
+  *mul_b = B > 1 && s[0] ? 1 : 0;
+  *mul_h = H > 1 && s[1] ? 1 : 0;
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)N, (uint64_t)(*mul_h ? H : 1),
+                            (uint64_t)(*mul_b ? B : 1)};
+  auto bytes = [&](int64_t st, bool on) { return on && st ? (uint64_t)st * 2 : (uint64_t)d * 2; };
+  const uint64_t strides[3] = {bytes(s[2], N > 1), bytes(s[1], *mul_h), bytes(s[0], *mul_b)};
+  for (uint64_t st : strides)
+    if (st >> 40) return false;
+  const uint32_t box[4] = {64, (uint32_t)rows, (uint32_t)heads, 1};
+  return encode_tmap(m, dt, 4, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename T, int D, bool SOLO, bool XF>
+cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                   const CUtensorMap& v, int sms, cudaStream_t st) {
+  auto kern = k_attend_masked<T, D, SOLO, XF>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  spr_launch(kern, a.n_items < sms ? a.n_items : sms, AM_THREADS, smem_bytes<D>(), st, q, k, v, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.partial) {
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+    spr_launch(k_am_join<T, D, SOLO>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_for(bool solo, const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                       const CUtensorMap& v, int sms, cudaStream_t st) {
+  const bool xf = a.softcap > 0.f || a.slopes;
+  if (solo)
+    return xf ? launch<T, D, true, true>(a, q, k, v, sms, st)
+              : launch<T, D, true, false>(a, q, k, v, sms, st);
+  return xf ? launch<T, D, false, true>(a, q, k, v, sms, st)
+            : launch<T, D, false, false>(a, q, k, v, sms, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -114,7 +860,8 @@ spr_status check(const spr_masked_params* p) {
   if (p->causal != 0 && p->causal != 1) return SPR_EINVAL;
   if (p->q_start != SPR_ALIGN_END && (p->q_start < -(1 << 30) || p->q_start > (1 << 30)))
     return SPR_EINVAL;
-  if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || p->B > 65535 || p->Hq > 65535)
+  if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || p->B > 65535 || p->Hq > 65535 ||
+      (int64_t)p->B * p->Hq * p->Nq > (1 << 30))
     return SPR_EUNSUPPORTED;
   if (!strides_fit(p->q_strides, p->B, p->Hq, p->Nq, false) ||
       !strides_fit(p->k_strides, p->B, p->Hk, p->Nk, false) ||
@@ -130,7 +877,7 @@ spr_status check(const spr_masked_params* p) {
 using namespace spr;
 
 extern "C" size_t sparsepr_attend_masked_workspace(const spr_masked_params* p) {
-  return check(p) == SPR_OK ? 256 : 0;
+  return check(p) == SPR_OK ? make_plan(*p, num_sms()).total : 0;
 }
 
 extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const void* Q,
@@ -148,23 +895,68 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
       !aligned(lse, 4) || !aligned(k_len, 4) || !aligned(doc_q, 4) || !aligned(doc_k, 4) ||
       !aligned(prefix, 4) || !aligned(slopes, 4) || !aligned(status, 4))
     return SPR_EUNSUPPORTED;
-  AmArgs a{Q, K, V, O, lse, k_len, doc_q, doc_k, prefix, slopes, {}, {}, {}, {}, p->B, p->Hq, p->Hk,
-           p->Nq, p->Nk, p->causal, p->q_start, 0.f, p->softcap};
-  for (int i = 0; i < 3; ++i) {
-    a.qs[i] = p->q_strides[i];
-    a.ks[i] = p->k_strides[i];
-    a.vs[i] = p->v_strides[i];
-    a.os[i] = p->o_strides[i];
-  }
+  const int sms = num_sms();
+  const Plan q = make_plan(*p, sms);
+  AmArgs a{};
+  a.O = O;
+  a.lse = lse;
+  a.k_len = k_len;
+  a.doc_q = doc_q;
+  a.doc_k = doc_k;
+  a.prefix = prefix;
+  a.slopes = slopes;
+  for (int i = 0; i < 3; ++i) a.os[i] = p->o_strides[i];
+  a.B = p->B;
+  a.Hq = p->Hq;
+  a.Hk = p->Hk;
+  a.Nq = p->Nq;
+  a.Nk = p->Nk;
+  a.causal = p->causal;
+  a.q_start = p->q_start;
   a.scale = p->scale > 0.f ? p->scale : 1.f / sqrtf((float)p->d);
+  a.softcap = p->softcap;
+  a.pack = q.pack;
+  a.ntile_h = q.ntile_h;
+  a.nqb = q.nqb;
+  a.nsplit = q.nsplit;
+  a.n_items = q.n_items;
+  a.partial = q.solo || q.nsplit > 1;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int32_t* count = reinterpret_cast<int32_t*>(base + q.count_off);
+  int32_t* list = reinterpret_cast<int32_t*>(base + q.list_off);
+  a.doc_count = count;
+  a.doc_list = list;
+  a.ktiles = q.ktiles;
+  a.part_o = reinterpret_cast<float*>(base + q.o_off);
+  a.part_ml = reinterpret_cast<float*>(base + q.ml_off);
+  a.part_rows = q.part_rows;
+  a.status = status;
+  const CUtensorMapDataType dt = p->dtype == SPR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap mq, mk, mv;
+  if (!tmap_available()) return SPR_ECUDA;
+  if (!make_map(&mq, Q, dt, p->B, p->Hq, p->Nq, p->d, p->q_strides, q.pack > 1 ? p->Nq : TBM,
+                q.pack, &a.qmul_b, &a.qmul_h) ||
+      !make_map(&mk, K, dt, p->B, p->Hk, p->Nk, p->d, p->k_strides, TBN, 1, &a.kmul_b, &a.kmul_h) ||
+      !make_map(&mv, V, dt, p->B, p->Hk, p->Nk, p->d, p->v_strides, TBN, 1, &a.vmul_b, &a.vmul_h))
+    return SPR_EUNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (status && cudaMemsetAsync(status, 0, 4 * sizeof(int32_t), st) != cudaSuccess)
     return SPR_ECUDA;
-  const dim3 grid((a.Nq + 31) / 32, a.Hq, a.B);
-  auto go = [&](auto kern) { spr_launch(kern, grid, 256, 0, st, a); };
+  if (doc_q) {
+    const dim3 grid(q.nqb, p->B);
+    if (q.solo)
+      spr_launch(k_am_documents<true>, grid, 1024, 0, st, a, count, list);
+    else
+      spr_launch(k_am_documents<false>, grid, 1024, 0, st, a, count, list);
+    if (cudaGetLastError() != cudaSuccess) return SPR_ECUDA;
+  }
+  cudaError_t e;
   if (p->dtype == SPR_BF16)
-    p->d == 64 ? go(k_attend_simple<bf16, 64>) : go(k_attend_simple<bf16, 128>);
+    e = p->d == 64 ? launch_for<bf16, 64>(q.solo, a, mq, mk, mv, sms, st)
+                   : launch_for<bf16, 128>(q.solo, a, mq, mk, mv, sms, st);
   else
-    p->d == 64 ? go(k_attend_simple<__half, 64>) : go(k_attend_simple<__half, 128>);
-  return cudaGetLastError() == cudaSuccess ? SPR_OK : SPR_ECUDA;
+    e = p->d == 64 ? launch_for<__half, 64>(q.solo, a, mq, mk, mv, sms, st)
+                   : launch_for<__half, 128>(q.solo, a, mq, mk, mv, sms, st);
+  return e == cudaSuccess ? SPR_OK : SPR_ECUDA;
 }
