@@ -863,7 +863,8 @@ spr_status check(const spr_masked_params* p) {
   if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || p->B > 65535 || p->Hq > 65535 ||
       (int64_t)p->B * p->Hq * p->Nq > (1 << 30))
     return SPR_EUNSUPPORTED;
-  if (!strides_fit(p->q_strides, p->B, p->Hq, p->Nq, false) ||
+  // (Q's too: packed heads are one box of its tensor map)
+  if (!strides_fit(p->q_strides, p->B, p->Hq, p->Nq, true) ||
       !strides_fit(p->k_strides, p->B, p->Hk, p->Nk, false) ||
       !strides_fit(p->v_strides, p->B, p->Hk, p->Nk, false) ||
       !strides_fit(p->o_strides, p->B, p->Hq, p->Nq, true))
