@@ -41,8 +41,8 @@ constexpr int TBM = 128, TBN = 128;  // query rows of a stream, keys of a tile
 constexpr uint32_t BOX = TBN * 128;  // one swizzled box of 128 rows x 64 channels: 16 KB
 constexpr int AM_THREADS = 384;      // two softmax warpgroups; a loading, an issuing and two idle warps
 // Registers: 168 a thread at launch (64,512 in all); a softmax thread holds a row of 128 scores.
-// 2 x 128 x 208 + 128 x 88 = 64,512.
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+// 2 x 128 x 200 + 128 x 104 = 64,512.
+constexpr int SOFTMAX_REGS = 200, OTHER_REGS = 104;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S0 | S1 | O0 | O1, 128 columns each
 constexpr uint64_t WAIT_NS = 2000000000ull;  // 2 s
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
@@ -51,9 +51,10 @@ template <int D>
 __host__ __device__ constexpr uint32_t tile_bytes() { return TBN * D * 2; }
 template <int D>
 __host__ __device__ constexpr int ring() { return D == 128 ? 5 : 8; }  // K and V tiles in flight
+// (the last 1024: barriers and the ring of items)
 template <int D>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return 1024 + (2 + ring<D>()) * (size_t)tile_bytes<D>() + 512;
+  return 1024 + (2 + ring<D>()) * (size_t)tile_bytes<D>() + 1024;
 }
 
 struct AmArgs {
@@ -66,9 +67,10 @@ struct AmArgs {
   int qmul_b, qmul_h, kmul_b, kmul_h, vmul_b, vmul_h;  // 0 where a TMA dimension has one entry
   float scale, softcap;
   // the plan: tiles of rows (heads packed per tile `pack`, query blocks `nqb`), key splits
-  int pack, ntile_h, nqb, nsplit, n_items, partial;
+  int pack, ntile_h, nqb, nsplit, n_items, partial, by_block;
   // workspace: per row tile its listed key tiles (documents), partial results
   const int32_t *doc_count, *doc_list;
+  int* next_item;  // counter of the items taken, or null: a fixed share for each block
   int ktiles;
   float *part_o, *part_ml;
   int part_rows;  // rows of a row tile that partial results hold
@@ -90,39 +92,50 @@ struct Limits {
   }
 };
 
-// One work item: a row tile (or pair of them) and its share of the key tiles.
+// One work item: a row tile (or pair of them) and its share of the key tiles.  The
+// loading thread makes it and passes it on through a ring in shared memory.
 template <bool SOLO>
 struct Item {
-  int b, h0, q0, tile;       // batch, first query head, first query row, row tile (b, h, block)
-  int nt0, nt1;              // key tiles each stream visits
-  int i0, n;                 // first entry and entries of this item's list
-  const int32_t* list;       // documents: the listed tiles
+  int b, h0, q0;       // batch, first query head, first query row
+  int n, i0;           // key tiles of the item (-1: no more items) and the first of them
+  int nt[2];           // key tiles each stream visits, from key 0 on
+  int last[2];         // entry after which a stream has no more tiles, at the latest
+  int near;            // with a distance penalty: the tile of the rows' position, else -1
+  int64_t part;        // its first partial result
+  const int32_t* list; // documents: the listed tiles
   Limits lim;
   __device__ void init(const AmArgs& a, int item) {
-    const int split = item % a.nsplit;
-    tile = item / a.nsplit;
-    const int blk = tile % a.nqb;
-    int t = tile / a.nqb;
+    const int split = item % a.nsplit, at = item / a.nsplit, heads = a.B * a.ntile_h;
+    const int blk = a.by_block ? at / heads : at % a.nqb;
+    int t = a.by_block ? at % heads : at / a.nqb;
+    part = (int64_t)((t * a.nqb + blk) * a.nsplit + split) * 2;
     const int ht = t % a.ntile_h;
     b = t / a.ntile_h;
     // heads: `pack` query heads per tile within a key head
     const int rep = a.Hq / a.Hk, per = (rep + a.pack - 1) / a.pack;
     h0 = (ht / per) * rep + (ht % per) * a.pack;
     // blocks with the most keys first: later items then even out the SMs
+    // (across all heads with by_block)
     q0 = (a.causal ? a.nqb - 1 - blk : blk) * (SOLO ? TBM : 2 * TBM);
     lim.init(a, b);
-    nt0 = tiles(a, 0);
-    nt1 = SOLO ? nt0 : tiles(a, 1);
-    int most = max(nt0, nt1);
+    nt[0] = tiles(a, 0);
+    nt[1] = SOLO ? nt[0] : tiles(a, 1);
+    int most = max(nt[0], nt[1]);
     list = nullptr;
+    // Nearest keys first: their scores are the highest, so the maximum seldom moves.
+    near = a.slopes ? min(max((lim.pos0 + q0 + (SOLO ? 0 : TBM)) / TBN, -1), most - 1) : -1;
+    for (int s = 0; s < 2; ++s) last[s] = nt[s] - 1 > near ? nt[s] - 1 : near;
     if (a.doc_q) {
-      const int64_t at = (int64_t)b * a.nqb + q0 / (SOLO ? TBM : 2 * TBM);
-      list = a.doc_list + at * a.ktiles;
-      most = a.doc_count[at];
+      const int64_t row = (int64_t)b * a.nqb + q0 / (SOLO ? TBM : 2 * TBM);
+      list = a.doc_list + row * a.ktiles;
+      most = a.doc_count[4 * row];
+      last[0] = a.doc_count[4 * row + 1];
+      last[1] = a.doc_count[4 * row + 2];
     }
     const int share = (most + a.nsplit - 1) / a.nsplit;
     i0 = min(most, split * share);
     n = min(most, i0 + share) - i0;
+    for (int s = 0; s < 2; ++s) last[s] = SOLO ? n - 1 : min(last[s] - i0, n - 1);
   }
   __device__ __forceinline__ int tiles(const AmArgs& a, int s) const {
     const int first = q0 + s * TBM, last = min(first + TBM, a.Nq) - 1;
@@ -136,17 +149,19 @@ struct Item {
       bits = e & 31;
       return e >> 5;
     }
-    const int t = i0 + i;
-    bits = 12 | (t < nt0 ? 1 : 0) | (t < nt1 ? 2 : 0) | ((t + 1) * TBN > lim.len ? 16 : 0);
+    int t = i0 + i;
+    if (t <= near) t = near - t;  // the rows' own tile first, then back, then on
+    bits = 12 | (t < nt[0] ? 1 : 0) | (t < nt[1] ? 2 : 0) | ((t + 1) * TBN > lim.len ? 16 : 0);
     return t;
   }
-  __device__ __forceinline__ bool visits(int i, int s) const {
-    if (SOLO) return (i & 1) == s;
+  __device__ __forceinline__ uint32_t streams(int i) const {
     int bits;
     entry(i, bits);
-    return bits >> s & 1;
+    return bits & 3;
   }
 };
+
+constexpr int ITEMS = 4;  // items in the ring
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -167,6 +182,30 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
 }
+// (a0, a1) * b + (c0, c1)
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0,
+                                     float c1) {
+  asm("{\n.reg .b64 ra, rb, rc, rd;\n"
+      "mov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\nmov.b64 rc, {%5, %6};\n"
+      "fma.rn.ftz.f32x2 rd, ra, rb, rc;\nmov.b64 {%0, %1}, rd;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+// (d0, d1) * (a0, a1) + c
+__device__ __forceinline__ void fma2e(float& d0, float& d1, float a0, float a1, float c) {
+  asm("{\n.reg .b64 ra, rc, rd;\n"
+      "mov.b64 ra, {%2, %3};\nmov.b64 rc, {%4, %4};\nmov.b64 rd, {%0, %1};\n"
+      "fma.rn.ftz.f32x2 rd, rd, ra, rc;\nmov.b64 {%0, %1}, rd;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(c));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 ra, rb, rd;\n"
+      "mov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %5};\n"
+      "mul.rn.ftz.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -180,6 +219,97 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Scores of a row, capped, in units of log 2: with z = x kz the score over the cap
+// (kz = scale / c), c tanh(z) = x scale (tanh(z) / z).  Where |z| <= 3/4 in all of
+// the tile's scores the quotient is a polynomial in z^2 (fitted for least error,
+// 2^-25 relative): 9 packed operations for two scores, none on the multi-function
+// unit.  False, with x spoiled, where a score lies beyond.
+__device__ __forceinline__ bool cap_near(float* x, float kz, float scale) {
+  float far[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < TBN; k += 2) {
+    float z0, z1, u0, u1, p0, p1;
+    mul2(z0, z1, x[k], x[k + 1], kz, kz);
+    mul2(u0, u1, z0, z1, z0, z1);
+    far[(k >> 1) & 3] = max3(far[(k >> 1) & 3], u0, u1);
+    fma2(p0, p1, u0, u1, -0.004789074882864952f, 0.019691824913024902f, 0.019691824913024902f);
+    fma2e(p0, p1, u0, u1, -0.053403016179800034f);
+    fma2e(p0, p1, u0, u1, 0.1332675963640213f);
+    fma2e(p0, p1, u0, u1, -0.33333081007003784f);
+    fma2e(p0, p1, u0, u1, 1.f);
+    mul2(x[k], x[k + 1], x[k], x[k + 1], scale, scale);
+    mul2(x[k], x[k + 1], x[k], x[k + 1], p0, p1);
+  }
+  const bool beyond = max3(fmaxf(far[0], far[1]), far[2], far[3]) > 0.5625f;
+  return !__any_sync(0xffffffffu, beyond);
+}
+// The same for any scores: c tanh(z) = c - 2 c / (1 + e^(2 z)), zin = 2 kz log2 e and
+// cl = c log2 e.
+__device__ __forceinline__ void cap_far(float* x, float zin, float cl) {
+#pragma unroll
+  for (int k = 0; k < TBN; ++k) x[k] = fmaf(-2.f * cl, rcp(1.f + ex2(x[k] * zin)), cl);
+}
+// Scores times `scale`, less the slope times the distance |at - k| of key k.  The
+// distance of a tile that lies wholly before or behind the row is linear in k.
+__device__ __forceinline__ void bias_scores(float* x, float scale, float slope, float at) {
+  if (__all_sync(0xffffffffu, at >= (float)(TBN - 1) || at <= 0.f)) {
+    const float ns = at > 0.f ? -slope : slope;
+    float d0 = at, d1 = at - 1.f;
+#pragma unroll
+    for (int k = 0; k < TBN; k += 2) {
+      float y0, y1;
+      mul2(y0, y1, x[k], x[k + 1], scale, scale);
+      fma2(x[k], x[k + 1], d0, d1, ns, y0, y1);
+      add2(d0, d1, -2.f, -2.f);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < TBN; ++k) x[k] = fmaf(-slope, fabsf(at - (float)k), x[k] * scale);
+}
+
+// Which of a tile's 128 keys a row sees (bit k of word k / 32): those below its
+// limit and, with documents, of its document.  The rows of a warp carry few
+// documents as a rule: one ballot per document and word serves all its rows.
+__device__ __forceinline__ void seen_keys(uint32_t* seen, int left, bool docs, const int32_t* doc_k,
+                                          int t0, int Nk, int docq) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = left - 32 * k;
+    seen[k] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  }
+  if (!docs) return;
+  int id[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) id[k] = __ldg(doc_k + min(t0 + 32 * k + lane, Nk - 1));
+  uint32_t todo = __ballot_sync(0xffffffffu, left > 0 && docq >= 0);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  while (todo) {
+    const int d = __shfl_sync(0xffffffffu, docq, __ffs(todo) - 1);
+    const bool same = docq == d;
+    todo &= ~__ballot_sync(0xffffffffu, same);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t on = __ballot_sync(0xffffffffu, id[k] == d);
+      if (same) w[k] = on;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) seen[k] &= w[k];
+}
+
+__device__ __forceinline__ float max_of(const float* x) {
+  float m[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m[e] = fmaxf(x[e], x[e + 8]);
+#pragma unroll
+  for (int k = 16; k < TBN; k += 16)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[e] = max3(m[e], x[k + e], x[k + 8 + e]);
+  return fmaxf(max3(m[0], m[1], m[2]), max3(max3(m[3], m[4], m[5]), m[6], m[7]));
 }
 
 // fp16 probabilities are scaled by 2^7: with the stale maximum they reach 2^15,
@@ -203,13 +333,17 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* s_full = bars + 2;   // [2]
-  uint64_t* p_full = bars + 4;   // [2]
-  uint64_t* o_full = bars + 6;   // [2]
-  uint64_t* o_free = bars + 8;   // [2]
-  uint64_t* drain = bars + 10;
-  uint64_t* full = bars + 11;          // [NST]
-  uint64_t* empty = bars + 11 + NST;   // [NST]
-  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(bars + 11 + 2 * NST);
+  uint64_t* p_full = bars + 4;   // [2] all of P
+  uint64_t* p_half = bars + 6;   // [2] P of the tile's first 64 keys
+  uint64_t* o_full = bars + 8;   // [2]
+  uint64_t* o_free = bars + 10;  // [2]
+  uint64_t* drain = bars + 12;
+  uint64_t* full = bars + 13;          // [NST]
+  uint64_t* empty = bars + 13 + NST;   // [NST]
+  uint64_t* it_full = bars + 13 + 2 * NST;          // [ITEMS]
+  uint64_t* it_empty = it_full + ITEMS;             // [ITEMS] eight softmax warps, the issuing warp
+  Item<SOLO>* ring_items = reinterpret_cast<Item<SOLO>*>(it_empty + ITEMS);
+  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(ring_items + ITEMS);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_base_s + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,10 +353,15 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(s_full + s, 1);
       tc::mbar_init(p_full + s, TBM);
+      tc::mbar_init(p_half + s, TBM);
       tc::mbar_init(o_full + s, 1);
       tc::mbar_init(o_free + s, TBM);
     }
     tc::mbar_init(drain, 1);
+    for (int s = 0; s < ITEMS; ++s) {
+      tc::mbar_init(it_full + s, 1);
+      tc::mbar_init(it_empty + s, 9);
+    }
     for (int s = 0; s < NST; ++s) {
       tc::mbar_init(full + s, 1);
       tc::mbar_init(empty + s, 1);
@@ -239,6 +378,17 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   tc::tc_fence_after();
   const uint32_t tbase = *tmem_base_s;
 
+  // Item k of this block, as a warp of the consumers sees it; false: no more.
+  auto next_item = [&](int k, Item<SOLO>& it) {
+    const bool got = tc::mbar_wait(it_full + k % ITEMS, (k / ITEMS) & 1, abort_s, WAIT_NS);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, got)) return false;
+    it = ring_items[k % ITEMS];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(it_empty + k % ITEMS);
+    return it.n >= 0;
+  };
+
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(OTHER_REGS));
   if (warp == 8) {
@@ -251,9 +401,21 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       bool ok = true;
       const uint32_t qbox = a.pack > 1 ? (uint32_t)(a.pack * a.Nq) * 128u : BOX;
       const int rep = a.Hq / a.Hk;
-      for (int w = blockIdx.x; w < a.n_items && ok; w += gridDim.x) {
+      for (int k = 0; ok; ++k) {
+        // blocks take the items forward and backward in turn, or whichever is next
+        const int w = a.next_item ? atomicAdd(a.next_item, 1)
+                            : k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         Item<SOLO> it;
-        it.init(a, w);
+        if (w < a.n_items)
+          it.init(a, w);
+        else
+          it.n = -1;
+        if (k >= ITEMS && !(ok = tc::mbar_wait(it_empty + k % ITEMS, ((k / ITEMS) - 1) & 1, abort_s,
+                                               WAIT_NS)))
+          break;
+        ring_items[k % ITEMS] = it;
+        tc::mbar_arrive(it_full + k % ITEMS);
+        if (it.n < 0) break;
         if (it.n == 0) continue;
         auto load_kv = [&](const CUtensorMap* m, int t, int mb, int mh) {
           const int s = c % NST;
@@ -293,101 +455,122 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr bool BF = std::is_same<T, bf16>::value;
-      constexpr uint32_t idS = BF ? tc::idesc_bf16(TBM, TBN, 0) : tc::idesc_fp16(TBM, TBN, 0);
-      constexpr uint32_t idPV = BF ? tc::idesc_bf16(TBM, D, 1) : tc::idesc_fp16(TBM, D, 1);
-      const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t kd = tc::smem_desc_sw128(smem_u32(sKV), 16, 1024);
-      const uint64_t vd = tc::smem_desc_sw128(smem_u32(sKV), BOX, 1024);
-      int c = 0;                     // ring entries of the items before this one
-      int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, items finished, per stream
-      int items = 0;
-      auto wait_ring = [&](int k) {
-        return tc::mbar_wait(full + k % NST, (k / NST) & 1, abort_s, WAIT_NS);
-      };
-      auto issue_s = [&](int s, int k) {
-        tc::tc_fence_after();
-        const uint64_t q = qd + (SOLO ? 0 : (uint64_t)(s * (TILE >> 4)));
-        const uint64_t b = kd + (uint64_t)((k % NST) * (TILE >> 4));
+    // All lanes run the loop, one issues: a run of products whose operands come
+    // from uniform registers costs the issuing thread less than the tensor core
+    // (a lane-0 branch made it the bound: 1,720 cycles to issue a stream's tile
+    // of 1,024 cycles of products).
+    constexpr bool BF = std::is_same<T, bf16>::value;
+    constexpr uint32_t idS = BF ? tc::idesc_bf16(TBM, TBN, 0) : tc::idesc_fp16(TBM, TBN, 0);
+    constexpr uint32_t idPV = BF ? tc::idesc_bf16(TBM, D, 1) : tc::idesc_fp16(TBM, D, 1);
+    const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t kd = tc::smem_desc_sw128(smem_u32(sKV), 16, 1024);
+    const uint64_t vd = tc::smem_desc_sw128(smem_u32(sKV), BOX, 1024);
+    int c = 0;                           // ring entries of the items before this one
+    int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles consumed, items finished, per stream
+    int items = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = tc::mbar_wait(bar, parity, abort_s, WAIT_NS);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    auto wait_ring = [&](int k) { return wait(full + k % NST, (k / NST) & 1); };
+    auto commit = [&](uint64_t* bar) {
+      if (tc::elect_one()) tc::mma_commit(bar);
+      __syncwarp();
+    };
+    auto issue_s = [&](int s, int k) {
+      tc::tc_fence_after();
+      const uint64_t q = qd + (SOLO ? 0 : (uint64_t)(s * (TILE >> 4)));
+      const uint64_t b = kd + (uint64_t)((k % NST) * (TILE >> 4));
+      if (tc::elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * BOX + (ks & 3) * 32) >> 4;
           tc::mma_ss(tbase + s * 128, q + off, b + off, idS, ks > 0);
         }
         tc::mma_commit(s_full + s);
-      };
-      auto issue_pv = [&](int s, int k, bool first) {
-        tc::tc_fence_after();
-        const uint64_t b = vd + (uint64_t)((k % NST) * (TILE >> 4));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int s, int k, auto half, uint32_t accumulate) {
+      tc::tc_fence_after();
+      const uint64_t b = vd + (uint64_t)((k % NST) * (TILE >> 4));
+      constexpr int K0 = decltype(half)::value * (TBN / 32);
+      if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < TBN / 16; ++kk)
+        for (int kk = K0; kk < K0 + TBN / 32; ++kk)
           tc::mma_ts(tbase + O_COL + s * 128, tbase + s * 128 + kk * 8, b + kk * (2048 >> 4), idPV,
-                     !(first && kk == 0));
-      };
-      bool ok = true;
-      for (int w = blockIdx.x; w < a.n_items && ok; w += gridDim.x) {
-        Item<SOLO> it;
-        it.init(a, w);
-        if (it.n == 0) continue;
-        if (!(ok = tc::mbar_wait(q_full, items & 1, abort_s, WAIT_NS))) break;
-        bool first[2] = {true, true};
-        // the first tile's scores (SOLO: of both streams' first tiles)
-        if (!(ok = wait_ring(c))) break;
-        if (SOLO || it.visits(0, 0)) issue_s(0, c);
-        if (!SOLO && it.visits(0, 1)) issue_s(1, c);
-        tc::mma_commit(empty + c % NST);
-        if (SOLO && it.n > 1) {
-          if (!(ok = wait_ring(c + 2))) break;
-          issue_s(1, c + 2);
-          tc::mma_commit(empty + (c + 2) % NST);
-        }
-        constexpr int AHEAD = SOLO ? 2 : 1;  // tiles between a stream's product and its next scores
-        if (it.n <= AHEAD) tc::mma_commit(q_empty);
-        for (int i = 0; i < it.n && ok; ++i) {
-          const int kv = c + 2 * i + 1, kn = c + 2 * (i + AHEAD);
-          const bool more = i + AHEAD < it.n;
-          if (!(ok = wait_ring(kv))) break;
-          bool have_k = false;
+                     kk == 0 ? accumulate : 1u);
+      }
+      __syncwarp();
+    };
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Item<SOLO> it;
+      if (!next_item(k, it)) break;
+      if (it.n == 0) continue;
+      if (!(ok = wait(q_full, items & 1))) break;
+      bool first[2] = {true, true}, done[2] = {false, false};
+      // the first tile's scores (SOLO: of both streams' first tiles)
+      if (!(ok = wait_ring(c))) break;
+      uint32_t on = it.streams(0), on_next;  // the streams that visit tile i and tile i + AHEAD
+      if (SOLO || (on & 1)) issue_s(0, c);
+      if (!SOLO && (on & 2)) issue_s(1, c);
+      commit(empty + c % NST);
+      if (SOLO && it.n > 1) {
+        if (!(ok = wait_ring(c + 2))) break;
+        issue_s(1, c + 2);
+        commit(empty + (c + 2) % NST);
+      }
+      constexpr int AHEAD = SOLO ? 2 : 1;  // tiles between a stream's product and its next scores
+      if (it.n <= AHEAD) commit(q_empty);
+      for (int i = 0; i < it.n; ++i, on = on_next) {
+        const int kv = c + 2 * i + 1, kn = c + 2 * (i + AHEAD);
+        const bool more = i + AHEAD < it.n;
+        if (SOLO) on = 1u << (i & 1);
+        on_next = SOLO ? on : more ? it.streams(i + AHEAD) : 0u;
+        if (!(ok = wait_ring(kv))) break;
+        bool have_k = false;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (!ok) break;
-            if (it.visits(i, s)) {
-              if (!(ok = tc::mbar_wait(p_full + s, np[s] & 1, abort_s, WAIT_NS))) break;
-              ++np[s];
-              if (first[s] && no[s] > 0 &&
-                  !(ok = tc::mbar_wait(o_free + s, (no[s] - 1) & 1, abort_s, WAIT_NS)))
-                break;
-              issue_pv(s, kv, first[s]);
-              first[s] = false;
-            }
-            if (more && it.visits(i + AHEAD, s)) {
-              if (!have_k && !(ok = wait_ring(kn))) break;
-              have_k = true;
-              issue_s(s, kn);
+        for (int s = 0; s < 2; ++s) {
+          if (on >> s & 1) {
+            if (!(ok = wait(p_half + s, np[s] & 1))) break;
+            if (first[s] && no[s] > 0 && !(ok = wait(o_free + s, (no[s] - 1) & 1))) break;
+            issue_pv(s, kv, std::integral_constant<int, 0>{}, !first[s]);
+            if (!(ok = wait(p_full + s, np[s] & 1))) break;
+            issue_pv(s, kv, std::integral_constant<int, 1>{}, 1u);
+            ++np[s];
+            first[s] = false;
+            if (!SOLO && i == it.last[s]) {
+              commit(o_full + s);
+              done[s] = true;
             }
           }
-          if (!ok) break;
-          tc::mma_commit(empty + kv % NST);
-          if (more) {
+          if (more && (on_next >> s & 1)) {
             if (!have_k && !(ok = wait_ring(kn))) break;
-            tc::mma_commit(empty + kn % NST);
-            if (i + AHEAD + 1 == it.n) tc::mma_commit(q_empty);
+            have_k = true;
+            issue_s(s, kn);
           }
         }
         if (!ok) break;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (!first[s]) {
-            tc::mma_commit(o_full + s);
-            ++no[s];
-          }
-        c += 2 * it.n;
-        ++items;
+        commit(empty + kv % NST);
+        if (more) {
+          if (!have_k && !(ok = wait_ring(kn))) break;
+          commit(empty + kn % NST);
+          if (i + AHEAD + 1 == it.n) commit(q_empty);
+        }
       }
-      tc::mma_commit(drain);
-      tc::mbar_wait_bounded(drain, 0, WAIT_NS);
+      if (!ok) break;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (!first[s]) {
+          if (SOLO || !done[s]) commit(o_full + s);
+          ++no[s];
+        }
+      c += 2 * it.n;
+      ++items;
     }
+    commit(drain);
+    tc::mbar_wait_bounded(drain, 0, WAIT_NS);
   }
   } else {
     // ------------------------------------------------------------ softmax
@@ -398,9 +581,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     const float scale_log2 = a.scale * LOG2E;
     int np = 0, no = 0, c = 0;  // tiles and items this stream has had, ring entries so far
     bool ok = true;
-    for (int w = blockIdx.x; w < a.n_items && ok; w += gridDim.x) {
+    for (int k = 0; ok; ++k) {
       Item<SOLO> it;
-      it.init(a, w);
+      if (!next_item(k, it)) break;
       // this thread's row: query head and query
       int h = it.h0, qi = it.q0 + (SOLO ? 0 : s * TBM) + row;
       bool live = qi < a.Nq;
@@ -415,12 +598,19 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       const int lim = live ? it.lim.limit(qi) : 0;
       const int docq = a.doc_q && live ? a.doc_q[(int64_t)it.b * a.Nq + qi] : 0;
       const float slope = XF && a.slopes ? a.slopes[h] * LOG2E : 0.f;
+      const int32_t* dk = a.doc_k ? a.doc_k + (int64_t)it.b * a.Nk : nullptr;
+      const bool work = __any_sync(0xffffffffu, live);  // a warp without rows only keeps step
       float m = -INFINITY, l = 0.f;
-      bool first = true;
+      bool first = true, far = false;
       for (int i = 0; i < it.n; ++i) {
         int bits;
         const int t = it.entry(i, bits);
         if (SOLO ? (i & 1) != s : !(bits >> s & 1)) continue;
+        const int t0 = t * TBN;
+        const bool doc_part = dk && !(bits >> (SOLO ? 2 : 2 + s) & 1);
+        const bool part = doc_part || t0 + TBN > whole;  // keys of the tile are hidden from rows
+        uint32_t seen[4];
+        if (part && work) seen_keys(seen, lim - t0, doc_part, dk, t0, a.Nk, docq);
         const bool got_s = tc::mbar_wait(s_full + s, np & 1, abort_s, WAIT_NS);
         __syncwarp();
         if (!__all_sync(0xffffffffu, got_s)) {
@@ -429,107 +619,112 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         }
         ++np;
         tc::tc_fence_after();
-        uint32_t sr[TBN];
+        float x[TBN];
+        auto load = [&]() {
+          uint32_t* sr = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc::tmem_ld32(scol + 32 * k, sr + 32 * k);
-        tc::tmem_wait_ld();
-        const int t0 = t * TBN;
-        float sl2 = scale_log2;
-        if (XF) {
-          if (a.softcap > 0.f) {  // c tanh(z) = c - 2 c / (1 + e^(2 z)), in units of log 2
-            const float zin = 2.f * scale_log2 / a.softcap, cl = a.softcap * LOG2E;
-#pragma unroll
-            for (int k = 0; k < TBN; ++k)
-              sr[k] = __float_as_uint(
-                  fmaf(-2.f * cl, rcp(1.f + ex2(__uint_as_float(sr[k]) * zin)), cl));
-          } else {
-#pragma unroll
-            for (int k = 0; k < TBN; ++k)
-              sr[k] = __float_as_uint(__uint_as_float(sr[k]) * scale_log2);
-          }
-          if (a.slopes) {
-            const float at = (float)(it.lim.pos0 + qi - t0);
-#pragma unroll
-            for (int k = 0; k < TBN; ++k)
-              sr[k] = __float_as_uint(
-                  fmaf(-slope, fabsf(at - (float)k), __uint_as_float(sr[k])));
-          }
-          sl2 = 1.f;
-        }
-        if (!(bits >> (SOLO ? 2 : 2 + s) & 1) || t0 + TBN > whole) {
-          const int left = lim - t0;
-#pragma unroll
-          for (int k = 0; k < TBN; ++k)
-            if (k >= left) sr[k] = __float_as_uint(-INFINITY);
-          if (a.doc_k && !(bits >> (SOLO ? 2 : 2 + s) & 1)) {
-            const int32_t* dk = a.doc_k + (int64_t)it.b * a.Nk;
-#pragma unroll
-            for (int k = 0; k < TBN; ++k) {
-              const int id = __ldg(dk + min(t0 + k, a.Nk - 1));
-              if (id != docq || id < 0) sr[k] = __float_as_uint(-INFINITY);
+          for (int k = 0; k < 4; ++k) tc::tmem_ld32(scol + 32 * k, sr + 32 * k);
+          tc::tmem_wait_ld();
+        };
+        auto take = [&]() {  // the row's scores, transformed and masked
+          load();
+          if (XF) {
+            const bool cap = a.softcap > 0.f;
+            if (cap) {
+              const float kz = a.scale / a.softcap;
+              if (!far && !cap_near(x, kz, scale_log2)) {
+                far = true;  // for the rest of the item: such scores seldom come alone
+                load();
+              }
+              if (far) cap_far(x, 2.f * LOG2E * kz, a.softcap * LOG2E);
             }
+            if (a.slopes || !cap)
+              bias_scores(x, cap ? 1.f : scale_log2, slope, (float)(it.lim.pos0 + qi - t0));
           }
-        }
-        float mx8[8];
+          if (part) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          mx8[e] = fmaxf(__uint_as_float(sr[e]), __uint_as_float(sr[e + 8]));
+            for (int k = 0; k < TBN; ++k)
+              if (!(seen[k / 32] & (1u << (k % 32)))) x[k] = -INFINITY;
+          }
+        };
+        const float sl2 = XF ? 1.f : scale_log2;
+        uint32_t pr[32];
+        float sum4[4];
+        // P of 64 keys from key K0 on.  A row that has seen nothing keeps m = -inf;
+        // what it adds up meanwhile is dropped with the first score it sees, or at the end.
+        auto exps = [&](auto from) {
+          constexpr int K0 = decltype(from)::value;
+          const float neg = m == -INFINITY ? 0.f : p_shift<T>() - m;
 #pragma unroll
-        for (int k = 16; k < TBN; k += 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mx8[e] = max3(mx8[e], __uint_as_float(sr[k + e]), __uint_as_float(sr[k + 8 + e]));
-        const float mx = fmaxf(max3(mx8[0], mx8[1], mx8[2]),
-                               max3(max3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])) * sl2;
-        const float mn = fmaxf(m, mx);
-        float m_use = m;
-        bool rescale = false;
-        if (mn > m + 8.f) {
-          m_use = mn;
-          rescale = !first;
-        }
-        const float corr = rescale ? ex2(m - m_use) : 1.f;
-        // a row that has seen nothing keeps m = -inf; its probabilities are 2^-inf = 0
-        const float neg = m_use == -INFINITY ? 0.f : p_shift<T>() - m_use;
-        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t pr[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 32; ++e) {
             float x0, x1;
-            fma2(x0, x1, __uint_as_float(sr[32 * k + 2 * e]), __uint_as_float(sr[32 * k + 2 * e + 1]),
-                 sl2, neg);
+            fma2(x0, x1, x[K0 + 2 * e], x[K0 + 2 * e + 1], sl2, neg);
             const float p0 = ex2(x0), p1 = ex2(x1);
             add2(sum4[2 * (e & 1)], sum4[2 * (e & 1) + 1], p0, p1);
             pr[e] = pack2<T>(p0, p1);
           }
-          __syncwarp();
-          tc::tmem_st16(scol + 16 * k, pr);
-        }
-        if (__any_sync(0xffffffffu, rescale)) {  // the products before S(i) are done: O is at rest
+        };
+        using Lo = std::integral_constant<int, 0>;
+        using Hi = std::integral_constant<int, TBN / 2>;
+        // A row's maximum is moved only when it grew by more than 2^8: then what was
+        // added up so far is scaled down.
+        auto move_max = [&](bool grown, float mx) {
+          const float top = grown ? mx : m;
+          if (!first) {  // the products before S(i) are done: O is at rest
+            const float corr = grown ? ex2(m - top) : 1.f;
+            l *= corr;
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
-            __syncwarp();
-            tc::tmem_ld32(ocol + 32 * k, o);
-            tc::tmem_wait_ld();
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t o[16];
+              __syncwarp();
+              tc::tmem_ld16(ocol + 16 * k, o);
+              tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            __syncwarp();
-            tc::tmem_st32(ocol + 32 * k, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              __syncwarp();
+              tc::tmem_st16(ocol + 16 * k, o);
+            }
+          }
+          m = top;
+        };
+        // XF: where every probability of the warp's rows would be flushed to 0 (a
+        // distance penalty far from the rows), there is no exponential to take.
+        bool nothing = false;
+        if (XF) {
+          if (work) {
+            take();
+            const float mx = max_of(x);
+            const bool grown = mx > m + 8.f;
+            if (__any_sync(0xffffffffu, grown)) move_max(grown, mx);
+            nothing = __all_sync(0xffffffffu, mx < m - 140.f);
+            sum4[0] = sum4[1] = sum4[2] = sum4[3] = 0.f;
+            if (nothing) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) pr[e] = 0u;
+            } else {
+              exps(Lo{});
+            }
+          }
+        } else {
+          // the first half's exponentials go ahead with the maximum so far, under
+          // the search for the new one; they are seldom taken again
+          while (work) {
+            take();
+            const float mx = max_of(x) * sl2;
+            sum4[0] = sum4[1] = sum4[2] = sum4[3] = 0.f;
+            exps(Lo{});
+            const bool grown = mx > m + 8.f;
+            if (!__any_sync(0xffffffffu, grown)) break;
+            move_max(grown, mx);
           }
         }
-        l = l * corr + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-        m = m_use;
         first = false;
+        bool got_v = true;
         if (bits & 16) {  // zero the V rows of keys that count for nobody
           const int kv = c + 2 * i + 1;
-          const bool got_v = tc::mbar_wait(full + kv % NST, (kv / NST) & 1, abort_s, WAIT_NS);
+          got_v = tc::mbar_wait(full + kv % NST, (kv / NST) & 1, abort_s, WAIT_NS);
           const int j = t0 + row;
-          const bool dead = j >= it.lim.len ||
-                            (a.doc_k && a.doc_k[(int64_t)it.b * a.Nk + j] < 0);
-          if (got_v && dead) {
+          if (got_v && (j >= it.lim.len || (dk && dk[j] < 0))) {
             uint8_t* v = sKV + (size_t)(kv % NST) * TILE + row * 128;
 #pragma unroll
             for (int k = 0; k < NBOX; ++k)
@@ -544,14 +739,27 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             break;
           }
         }
-        __syncwarp();
-        tc::tmem_wait_st();
+        if (work) {
+          __syncwarp();
+          tc::tmem_st32(scol, pr);
+          tc::tmem_wait_st();
+        }
+        tc::tc_fence_before();
+        tc::mbar_arrive(p_half + s);
+        if (work) {
+          if (!nothing) exps(Hi{});
+          __syncwarp();
+          tc::tmem_st32(scol + 32, pr);
+          l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          tc::tmem_wait_st();
+        }
         tc::tc_fence_before();
         tc::mbar_arrive(p_full + s);
       }
       if (!ok) break;
       c += 2 * it.n;
       const bool any = !first;
+      if (m == -INFINITY && l == l) l = 0.f;  // the row saw no key
       if (any) {
         const bool got_o = tc::mbar_wait(o_full + s, no & 1, abort_s, WAIT_NS);
         __syncwarp();
@@ -563,7 +771,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         tc::tc_fence_after();
       }
       if (a.partial) {
-        const int64_t part = ((int64_t)w * 2 + s) * a.part_rows + row;
+        const int64_t part = (it.part + s) * a.part_rows + row;
         if (live) {
           a.part_ml[2 * part] = m;
           a.part_ml[2 * part + 1] = l;
@@ -633,12 +841,16 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   }
 }
 
-// Add up the partial results of a row: a warp per row, parts = 2 nsplit.
-template <typename T, int D, bool SOLO>
+// Add up the partial results of a row: a block per JOIN_ROWS rows, JOIN_WARPS
+// warps to a row, each with every JOIN_WARPS-th of the row's parts (2 nsplit of
+// them in the SOLO form, nsplit in the other), in an order that is fixed.
+template <typename T, int D, bool SOLO, int WARPS>
 __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // (batch, head, query)
-  const int lane = threadIdx.x & 31;
-  if (r >= (int64_t)a.B * a.Hq * a.Nq) return;
+  constexpr int ROWS = 4 / WARPS, E = D / 32;
+  __shared__ float sm[4], sl[4], so[4][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+  const int64_t r = min((int64_t)blockIdx.x * ROWS + warp / WARPS, rows - 1);  // (batch, head, query)
   const int qi = (int)(r % a.Nq), h = (int)(r / a.Nq % a.Hq), b = (int)(r / a.Nq / a.Hq);
   const int rep = a.Hq / a.Hk, per = (rep + a.pack - 1) / a.pack;
   const int ht = h / rep * per + h % rep / a.pack;
@@ -650,13 +862,14 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
   const int np = SOLO ? 2 * a.nsplit : a.nsplit, step = SOLO ? 1 : 2;
   const int64_t p0 = (tile * a.nsplit * 2 + s) * a.part_rows + row;
   const int64_t pstep = (int64_t)step * a.part_rows;
+  const int first = warp % WARPS;
   float M = -INFINITY;
-  for (int p = lane; p < np; p += 32) M = fmaxf(M, a.part_ml[2 * (p0 + p * pstep)]);
+  for (int p = first + WARPS * lane; p < np; p += WARPS * 32)
+    M = fmaxf(M, a.part_ml[2 * (p0 + p * pstep)]);
   M = warp_max(M);
-  constexpr int E = D / 32;
   float o[E] = {}, l = 0.f;
 #pragma unroll 4
-  for (int p = 0; p < np; ++p) {
+  for (int p = first; p < np; p += WARPS) {
     const int64_t at = p0 + p * pstep;
     const float m = a.part_ml[2 * at], lp = a.part_ml[2 * at + 1];
     if (lp == 0.f) continue;  // saw nothing; its O is not written
@@ -664,6 +877,27 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
     l += w * lp;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(w, a.part_o[at * D + E * lane + e], o[e]);
+  }
+  if (WARPS > 1) {
+    if (lane == 0) sm[warp] = M, sl[warp] = l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][E * lane + e] = o[e];
+    __syncthreads();
+    if (first) return;
+    float top = M;
+    for (int i = 1; i < WARPS; ++i) top = fmaxf(top, sm[warp + i]);
+    float w = M == -INFINITY ? 0.f : ex2(M - top);
+    l *= w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= w;
+    for (int i = 1; i < WARPS; ++i) {
+      if (sm[warp + i] == -INFINITY && sl[warp + i] == 0.f) continue;
+      w = ex2(sm[warp + i] - top);
+      l = fmaf(w, sl[warp + i], l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, so[warp + i][E * lane + e], o[e]);
+    }
+    M = top;
   }
   const float f = l != 0.f ? 1.f / l : 0.f;
   T* O = static_cast<T*>(a.O) + b * a.os[0] + h * a.os[1] + (int64_t)qi * a.os[2] + E * lane;
@@ -683,13 +917,14 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
 template <bool SOLO>
 __global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ AmArgs a,
                                                        int32_t* count, int32_t* list) {
-  __shared__ int lo[2], hi[2], neg[2], entry[32];
+  __shared__ int lo[2], hi[2], neg[2], final_entry[2], entry[32];
   const int b = blockIdx.y, blk = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int span = SOLO ? TBM : 2 * TBM, q0 = blk * span;
   if (threadIdx.x < 2) {
     lo[threadIdx.x] = INT32_MAX;
     hi[threadIdx.x] = -1;
     neg[threadIdx.x] = 0;
+    final_entry[threadIdx.x] = -1;
   }
   __syncthreads();
   if ((int)threadIdx.x < span && q0 + (int)threadIdx.x < a.Nq) {
@@ -746,19 +981,29 @@ __global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ A
     if (warp == 0) {
       const int e = entry[lane];
       const uint32_t keep = __ballot_sync(0xffffffffu, e >= 0);
-      if (e >= 0) out[n + __popc(keep & ((1u << lane) - 1))] = e;
+      if (e >= 0) {
+        const int slot = n + __popc(keep & ((1u << lane) - 1));
+        out[slot] = e;
+        if (e & 1) atomicMax(&final_entry[0], slot);
+        if (e & 2) atomicMax(&final_entry[1], slot);
+      }
       n += __popc(keep);
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) count[at] = n;
+  if (threadIdx.x == 0) {
+    count[4 * at] = n;
+    count[4 * at + 1] = final_entry[0];
+    count[4 * at + 2] = final_entry[1];
+    if (at == 0 && a.next_item) *a.next_item = 0;
+  }
 }
 
 // The plan of a call: which form, how many items, what the workspace holds.
 struct Plan {
   bool solo;
-  int pack, ntile_h, nqb, nsplit, n_items, ktiles, part_rows;
-  size_t count_off, list_off, o_off, ml_off, total;
+  int pack, ntile_h, nqb, nsplit, n_items, ktiles, part_rows, by_block;
+  size_t next_off, count_off, list_off, o_off, ml_off, total;
 };
 
 Plan make_plan(const spr_masked_params& p, int sms) {
@@ -772,12 +1017,28 @@ Plan make_plan(const spr_masked_params& p, int sms) {
   q.nqb = q.solo ? 1 : (p.Nq + 2 * TBM - 1) / (2 * TBM);
   q.ktiles = (p.Nk + TBN - 1) / TBN;
   const int64_t tiles = (int64_t)p.B * q.ntile_h * q.nqb;
-  q.nsplit = 1;
-  if (tiles < sms) {
-    const int most = (q.ktiles + 3) / 4;  // four key tiles a split at least
-    q.nsplit = (int)(sms / tiles) < most ? (int)(sms / tiles) : most;
-    if (q.nsplit < 1) q.nsplit = 1;
+  // Key splits with the least estimated time, in cycles of an SM: a key tile
+  // takes a SOLO block what its 4 d 128 bytes take at 24 bytes a cycle (the
+  // SM's share of HBM), the other form about 26 d cycles of softmax for its two
+  // streams; an item costs 2,000 or 4,000 cycles to start and end; the join a launch and
+  // the partial results' way out and back.  At least two tiles to a split.
+  const double step = q.solo ? 4.0 * p.d * TBN / 24 : 26.0 * p.d;
+  const double part = q.solo ? 2.0 * q.pack * p.Nq * p.d * 4 : 2.0 * TBM * p.d * 4;
+  const int most = q.ktiles / 2 < 1 ? 1 : q.ktiles / 2;
+  double best = 0;
+  for (int n = 1; n <= most && (n == 1 || tiles * n <= (q.solo ? 16 : 1) * (int64_t)sms); ++n) {
+    const int64_t rounds = (tiles * n + sms - 1) / sms;
+    const bool joined = q.solo || n > 1;
+    const double cost = (double)rounds * ((q.ktiles + n - 1) / n * step + (q.solo ? 2000.0 : 4000.0)) +
+                        (joined ? 6000.0 + 30.0 * n + 2.0 * tiles * n * part / 3500.0 : 0.0);
+    if (n == 1 || cost < best) {
+      best = cost;
+      q.nsplit = n;
+    }
   }
+  // Causal items differ in length: heaviest first over all heads, as long as
+  // the keys and values of all heads stay in L2 together.
+  q.by_block = p.causal && !q.solo && 4.0 * p.B * p.Hk * p.Nk * p.d <= 48e6;
   q.n_items = (int)(tiles * q.nsplit);
   q.part_rows = q.solo ? q.pack * p.Nq : TBM;
   size_t at = 0;
@@ -786,7 +1047,8 @@ Plan make_plan(const spr_masked_params& p, int sms) {
     at += (bytes + 255) / 256 * 256;
     return off;
   };
-  q.count_off = take((size_t)p.B * q.nqb * 4);
+  q.next_off = take(4);
+  q.count_off = take((size_t)p.B * q.nqb * 16);
   q.list_off = take((size_t)p.B * q.nqb * q.ktiles * 4);
   const bool partial = q.solo || q.nsplit > 1;
   q.o_off = take(partial ? (size_t)q.n_items * 2 * q.part_rows * p.d * 4 : 0);
@@ -822,7 +1084,11 @@ cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.partial) {
     const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-    spr_launch(k_am_join<T, D, SOLO>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
+    // a warp goes through four parts in about 1 us; few rows with many parts get four warps each
+    if ((SOLO ? 2 : 1) * a.nsplit > 8 && rows <= 65536)
+      spr_launch(k_am_join<T, D, SOLO, 4>, (unsigned)rows, 128, 0, st, a);
+    else
+      spr_launch(k_am_join<T, D, SOLO, 1>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
     e = cudaGetLastError();
   }
   return e;
@@ -920,12 +1186,17 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   a.ntile_h = q.ntile_h;
   a.nqb = q.nqb;
   a.nsplit = q.nsplit;
+  a.by_block = q.by_block;
   a.n_items = q.n_items;
   a.partial = q.solo || q.nsplit > 1;
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* count = reinterpret_cast<int32_t*>(base + q.count_off);
   int32_t* list = reinterpret_cast<int32_t*>(base + q.list_off);
   a.doc_count = count;
+  // Items of very different length are taken as blocks come free: documents, and
+  // lengths where each block has several items (the counter costs a memset).
+  const bool uneven = doc_q || (k_len && p->B > 1 && q.n_items > 2 * sms);
+  a.next_item = uneven && q.n_items > sms ? reinterpret_cast<int*>(base + q.next_off) : nullptr;
   a.doc_list = list;
   a.ktiles = q.ktiles;
   a.part_o = reinterpret_cast<float*>(base + q.o_off);
@@ -943,6 +1214,8 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
     return SPR_EUNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (status && cudaMemsetAsync(status, 0, 4 * sizeof(int32_t), st) != cudaSuccess)
+    return SPR_ECUDA;
+  if (a.next_item && !doc_q && cudaMemsetAsync(a.next_item, 0, 4, st) != cudaSuccess)
     return SPR_ECUDA;
   if (doc_q) {
     const dim3 grid(q.nqb, p->B);

@@ -226,6 +226,19 @@ __host__ __device__ constexpr uint32_t idesc_fp16(int M, int N, int b_mn) {
 // run-time trip count, a switch) slows the stream of products several-fold,
 // and a commit after every product costs about half a product; callers issue
 // each group of products as straight-line code and commit once per group.
+// One lane of a converged warp.  Products issued under it, by a warp whose lanes
+// all run the loop around them, take their descriptors from uniform registers;
+// under `lane == 0` every operand is moved there first, and the issuing thread
+// becomes the bound.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
 // D[tmem] (+)= A[smem desc] * B[smem desc]
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                        uint32_t idesc, uint32_t accumulate) {
