@@ -353,36 +353,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- products
-    if (lane == 0 && rank == 0) {
+    // All lanes of the first CTA's warp run the loop, one issues: the operands
+    // then come from uniform registers.
+    if (rank == 0) {
       const uint32_t id = std::is_same<T, bf16>::value ? tc::idesc_bf16(2 * PBM, a.bn, 0)
                                                        : tc::idesc_fp16(2 * PBM, a.bn, 0);
       const uint64_t xd = tc::smem_desc_sw128(smem_u32(sX), 16, 1024);
       const uint64_t wd = tc::smem_desc_sw128(smem_u32(sW), 16, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = tc::mbar_wait(bar, parity, abort_s, PJ_WAIT_NS);
+        return __all_sync(0xffffffffu, got) != 0;
+      };
       int c = 0, t = 0;
       bool ok = true;
       for (int w = first_item; w < a.n_items && ok; w += step) {
         const PjItem it(a, w);
         if (it.k0 == it.k1) continue;
         const uint32_t d = tbase + (t & 1) * 256;
-        if (t >= 2 && !(ok = tc::mbar_wait(acc_empty + (t & 1), ((t >> 1) - 1) & 1, abort_s,
-                                           PJ_WAIT_NS)))
-          break;
+        if (t >= 2 && !(ok = wait(acc_empty + (t & 1), ((t >> 1) - 1) & 1))) break;
         tc::tc_fence_after();
+        uint32_t more = 0;  // the tile's first product starts its sums
         for (int k = it.k0; k < it.k1; ++k, ++c) {
           const int s = c % NST;
-          if (!(ok = tc::mbar_wait(full + s, (c / NST) & 1, abort_s, PJ_WAIT_NS))) break;
+          if (!(ok = wait(full + s, (c / NST) & 1))) break;
           tc::tc_fence_after();
           const uint64_t at = (uint64_t)(s * (PBOX >> 4));
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < PBK / 16; ++i)
-            tc::mma_ss_pair(d, xd + at + 2 * i, wd + at + 2 * i, id, i > 0 || k > it.k0);
-          tc::mma_commit_pair(empty + s);
+            for (int i = 0; i < PBK / 16; ++i)
+              tc::mma_ss_pair(d, xd + at + 2 * i, wd + at + 2 * i, id, i > 0 ? 1u : more);
+            tc::mma_commit_pair(empty + s);
+            if (k + 1 == it.k1) tc::mma_commit_pair(acc_full + (t & 1));
+          }
+          __syncwarp();
+          more = 1;
         }
         if (!ok) break;
-        tc::mma_commit_pair(acc_full + (t & 1));
         ++t;
       }
-      tc::mma_commit_pair(drain);
+      if (tc::elect_one()) tc::mma_commit_pair(drain);
+      __syncwarp();
       tc::mbar_wait_bounded(drain, 0, PJ_WAIT_NS);
     }
   } else if (warp >= 4) {
