@@ -7,12 +7,14 @@ no CPU fallback: a missing library raises at load time.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libsparsepr.so")
+MARSHAL_PATH = os.path.join(_PKG, "lib", "_marshal.so")
 
 (SPR_OK, SPR_EINVAL, SPR_EUNSUPPORTED, SPR_EWORKSPACE, SPR_ECUDA, SPR_EDEVICE,
  SPR_ESCRATCH) = range(7)
@@ -101,7 +103,20 @@ EXPORTS = ["sparsepr_workspace_size", "sparsepr_check_params", "sparsepr_partiti
            "sparsepr_attend_masked", "sparsepr_attend_masked_workspace", "sparsepr_project",
            "sparsepr_project_workspace"]
 
-_lib = None
+_lib = _marshal = None
+
+
+def load_marshal():
+    """Load the extension module of the operators' calls once; raises if it has not been built."""
+    global _marshal
+    if _marshal is None:
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError(f"_marshal.so not built ({MARSHAL_PATH}); run "
+                               "`python -m free_block_sparse_means_b200.build`")
+        spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+        _marshal = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_marshal)
+    return _marshal
 
 
 def load_library(path: str = LIB_PATH):

@@ -1,10 +1,11 @@
-"""Build libsparsepr.so (sm_100a) in-tree with nvcc.
+"""Build libsparsepr.so (sm_100a) in-tree with nvcc, and the extension module _marshal with g++.
 
     python -m free_block_sparse_means_b200.build [--force] [--verbose]
 
 Objects go to _build/ at the repository root; the shared library goes to
 free_block_sparse_means_b200/lib/.  Rebuilds only when a source is newer than
-the library.
+the library.  _marshal (the operators' calls from Python, against the installed
+torch's headers) goes beside it.
 """
 from __future__ import annotations
 
@@ -21,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsparsepr.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(LIBDIR, "_marshal.so")
 BUILD = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -50,11 +53,51 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in sources() + headers() + [__file__])
 
 
+def marshal_command():
+    """The g++ command of _marshal; the process that loads it has torch's libraries already."""
+    import sysconfig
+
+    import torch
+    headers = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = [headers, os.path.join(headers, "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE,
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[a for i in inc for a in ("-isystem", i)], MARSHAL_SRC, "-o", MARSHAL + ".tmp",
+            "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def marshal_up_to_date() -> bool:
+    return os.path.exists(MARSHAL) and all(
+        os.path.getmtime(f) <= os.path.getmtime(MARSHAL)
+        for f in [MARSHAL_SRC, os.path.join(INCLUDE, "sparsepr.h"), __file__])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+    extension = None
     os.makedirs(LIBDIR, exist_ok=True)
+    if force or not marshal_up_to_date():
+        extension = subprocess.Popen(marshal_command(), stdout=subprocess.PIPE,
+                                     stderr=subprocess.STDOUT, text=True)
+    try:
+        if force or not up_to_date():
+            build_library(verbose)
+    finally:
+        if extension:
+            out, _ = extension.communicate()
+            if extension.returncode == 0:
+                os.replace(MARSHAL + ".tmp", MARSHAL)
+            else:
+                sys.stderr.write(out)
+    if extension and extension.returncode:
+        raise RuntimeError("g++ failed for: " + MARSHAL_SRC)
+    return LIB
+
+
+def build_library(verbose: bool) -> None:
+    os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     procs, objs = [], []
     for src in sources():
@@ -77,7 +120,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.check_call([cc, *ARCH, "-shared", "--cudart=static", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -5,7 +5,8 @@
 // k_project_few   At most FEW_ROWS rows: every weight is read once and used for
 //   a handful of rows, so the bound is reading W.  A warp streams 8 rows of W
 //   per load instruction straight into the B fragments of mma.sync (16 x 8 x 16,
-//   the rows of X are A); a block of 8 warps splits K and adds up in shared memory.
+//   the rows of X are A); the warps of a block split K and add up in shared memory.
+//   (32 rows this way: 38 us at 5,120 x 5,120, the other form 29 us.)
 //
 // k_project_pair  Everything else, on the 5th-generation tensor cores.  Two CTAs
 //   of a cluster make one tile of 256 rows x bn channels (cta_group::2): each
@@ -32,7 +33,7 @@
 namespace spr {
 namespace {
 
-constexpr int FEW_ROWS = 32;
+constexpr int FEW_ROWS = 16;
 constexpr int PBM = 128;                       // rows of a CTA's half of a tile
 constexpr int PBK = 64;                        // channels of a stage: one swizzled 128-byte row
 constexpr uint32_t PBOX = PBM * 128;           // 16 KB: 128 rows of 64 channels
@@ -159,85 +160,82 @@ __device__ __forceinline__ void mma_16816<__half>(float* d, const uint32_t* a, u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int FEW_THREADS = 256, FEW_WARPS = 8;
-constexpr int FEW_OUT = 16;     // channels of a block: two groups of 8 rows of W
-constexpr int FEW_UNROLL = 4;   // steps of 32 channels a warp has in flight
+constexpr int FEW_WARPS = 16;  // of a block, at most
 
 // A step: lane (g, q) holds 16 bytes, channels 8 q .. 8 q + 7, of row g of each
 // operand.  Taken as the fragments of two products (words 0, 1 and 2, 3) they
 // number the 32 channels in another order, the same one for X and W.
-template <typename T, int MT>
-__global__ void __launch_bounds__(FEW_THREADS) k_project_few(const __grid_constant__ PjArgs a) {
-  __shared__ float sums[FEW_WARPS][16 * MT][FEW_OUT + 1];
+// NG groups of 8 rows of X (the second is the lower half of A), NT groups of 8
+// rows of W, U steps in flight.
+template <typename T, int NG, int NT, int U>
+__global__ void __launch_bounds__(32 * FEW_WARPS) k_project_few(const __grid_constant__ PjArgs a) {
+  constexpr int OUT = 8 * NT;  // channels of a block
+  __shared__ float sums[FEW_WARPS][8 * NG][OUT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int m0 = blockIdx.x * FEW_OUT, rows = a.B * a.N;
-  const T* w[2];
-  bool has_w[2];
+  const int warps = blockDim.x >> 5;
+  const int m0 = blockIdx.x * OUT, rows = a.B * a.N;
+  const T* w[NT];
+  bool has_w[NT];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < NT; ++j) {
     const int m = m0 + 8 * j + g;
     has_w[j] = m < a.M;
     w[j] = static_cast<const T*>(a.W) + (int64_t)(has_w[j] ? m : 0) * a.ws;
   }
-  const T* x[2 * MT];
-  bool has_x[2 * MT];
+  const T* x[NG];
+  bool has_x[NG];
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) {
+  for (int i = 0; i < NG; ++i) {
     const int t = 8 * i + g;
     has_x[i] = t < rows;
     const int b = has_x[i] ? t / a.N : 0, n = has_x[i] ? t % a.N : 0;
     x[i] = static_cast<const T*>(a.X) + b * a.xs[0] + (int64_t)n * a.xs[2];
   }
-  float acc[MT][2][4] = {};
+  float acc[NT][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // this lane's channel and its place in X: head by head
   int k = warp * 32 + 8 * q, kx = k;
   int64_t head = 0;
-  for (; k - 8 * q < a.K; ) {
-    uint4 wv[FEW_UNROLL][2], xv[FEW_UNROLL][2 * MT];
+  while (k - 8 * q < a.K) {
+    uint4 wv[U][NT], xv[U][NG];
 #pragma unroll
-    for (int u = 0; u < FEW_UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const bool in = k < a.K;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) wv[u][j] = in && has_w[j] ? ld_stream(w[j] + k) : zero;
+      for (int j = 0; j < NT; ++j) wv[u][j] = in && has_w[j] ? ld_stream(w[j] + k) : zero;
       if (in)
         while (kx >= a.dx) {
           kx -= a.dx;
           head += a.xs[1];
         }
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i)
+      for (int i = 0; i < NG; ++i)
         xv[u][i] = in && has_x[i] ? __ldg(reinterpret_cast<const uint4*>(x[i] + head + kx)) : zero;
-      k += 32 * FEW_WARPS;
-      kx += 32 * FEW_WARPS;
+      k += 32 * warps;
+      kx += 32 * warps;
     }
 #pragma unroll
-    for (int u = 0; u < FEW_UNROLL; ++u)
+    for (int u = 0; u < U; ++u) {
+      const uint4 lo = xv[u][0], hi = NG > 1 ? xv[u][NG - 1] : zero;
+      const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const uint4 &lo = xv[u][2 * t], &hi = xv[u][2 * t + 1];
-        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mma_16816<T>(acc[t][j], a0, wv[u][j].x, wv[u][j].y);
-          mma_16816<T>(acc[t][j], a1, wv[u][j].z, wv[u][j].w);
-        }
+      for (int j = 0; j < NT; ++j) {
+        mma_16816<T>(acc[j], a0, wv[u][j].x, wv[u][j].y);
+        mma_16816<T>(acc[j], a1, wv[u][j].z, wv[u][j].w);
       }
+    }
   }
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sums[warp][16 * t + g + 8 * (e >> 1)][8 * j + 2 * q + (e & 1)] = acc[t][j][e];
+    for (int e = 0; e < 2 * NG; ++e)
+      sums[warp][g + 8 * (e >> 1)][8 * j + 2 * q + (e & 1)] = acc[j][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * FEW_OUT; i += FEW_THREADS) {
-    const int t = i / FEW_OUT, c = i % FEW_OUT, m = m0 + c;
+  for (int i = threadIdx.x; i < rows * OUT; i += blockDim.x) {
+    const int t = i / OUT, c = i % OUT, m = m0 + c;
     if (m >= a.M) continue;
     float v = 0.f;
-#pragma unroll
-    for (int s = 0; s < FEW_WARPS; ++s) v += sums[s][t][c];
+    for (int s = 0; s < warps; ++s) v += sums[s][t][c];
     if (a.bias) v += tof(static_cast<const T*>(a.bias)[m]);
     with_act(a.act, [&](auto act) { v = activate<decltype(act)::value>(v); });
     const int b = t / a.N, n = t % a.N, h = m / a.dy, ch = m - h * a.dy;
@@ -677,14 +675,24 @@ cudaError_t launch_pair(const PjArgs& a, const CUtensorMap& x, const CUtensorMap
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_few(const PjArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.M + FEW_OUT - 1) / FEW_OUT);
-  if (a.B * a.N <= 16)
-    spr_launch(k_project_few<T, 1>, grid, FEW_THREADS, 0, st, a);
-  else
-    spr_launch(k_project_few<T, 2>, grid, FEW_THREADS, 0, st, a);
+template <typename T, int NG, int NT, int U>
+cudaError_t launch_few(const PjArgs& a, int sms, cudaStream_t st) {
+  // Warps of a block: as many as make about 22 of them on every SM, each with a
+  // few rounds of its U steps at least.
+  const int blocks = (a.M + 8 * NT - 1) / (8 * NT), rounds = (a.K + 32 * U - 1) / (32 * U);
+  int warps = (22 * sms + blocks / 2) / blocks;
+  if (warps > rounds) warps = rounds;
+  warps = warps < 4 ? 4 : warps > FEW_WARPS ? FEW_WARPS : warps;
+  spr_launch(k_project_few<T, NG, NT, U>, blocks, 32 * warps, 0, st, a);
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_few(const PjArgs& a, int sms, cudaStream_t st) {
+  // Steps in flight: more of them cost more in resident warps than they bring (4 rows x
+  // 5,120 x 5,120: 2 steps 19.6 us, 3 16.6, 4 16.1, 6 25.2, 8 20.6; x 20,480: 53.9, 45.1,
+  // 52.0, 50.8, 49.2).  9 to 16 rows take two groups of 8 rows of W, so that X is read
+  // half as often (2 steps 16.5 us, 3 26.6, 4 31.2).
+  return a.B * a.N <= 8 ? launch_few<T, 1, 1, 3>(a, sms, st) : launch_few<T, 2, 2, 2>(a, sms, st);
 }
 
 }  // namespace
@@ -743,8 +751,8 @@ extern "C" spr_status sparsepr_project(const spr_project_params* p, const void* 
     return SPR_ECUDA;
   cudaError_t e;
   if (p->dtype == SPR_BF16)
-    e = few ? launch_few<bf16>(a, st) : launch_pair<bf16>(a, mx, mw, my, mr, sms, st);
+    e = few ? launch_few<bf16>(a, sms, st) : launch_pair<bf16>(a, mx, mw, my, mr, sms, st);
   else
-    e = few ? launch_few<__half>(a, st) : launch_pair<__half>(a, mx, mw, my, mr, sms, st);
+    e = few ? launch_few<__half>(a, sms, st) : launch_pair<__half>(a, mx, mw, my, mr, sms, st);
   return e == cudaSuccess ? SPR_OK : SPR_ECUDA;
 }

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from ._binding import (SprMaskedParams, SprNormRotateParams, SprProjectParams, _check,
-                       load_library)
+                       load_library, load_marshal)
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 PAIRINGS = {"interleaved": 0, "halves": 1}
@@ -49,25 +49,32 @@ def _option(name, value, table):
     return table[value]
 
 
-def _made(prm, **tensors):
-    """Keep with the parameters what the tensors they were made for look like, so that a call with
-    such tensors is checked by three comparisons each."""
-    prm.made_bytes = bytes(prm)
-    prm.made_for = {n: (tuple(t.shape), t.stride(), t.dtype) for n, t in tensors.items()
-                    if t is not None}
+def _made(prm, kind, where, *tensors):
+    """Keep with the parameters a plan of their calls: what the tensors they were made for look
+    like.  A call with such tensors is checked and made by the extension module in one step; any
+    other call, also one whose parameters were changed since, goes through the checks below."""
+    entry = ctypes.cast(getattr(load_library(), where), ctypes.c_void_p).value
+    prm.plan = load_marshal().plan(kind, ctypes.addressof(prm), ctypes.sizeof(prm), entry, tensors)
     return prm
 
 
-def _made_for(prm):
-    """What _made kept, as long as no field has been changed since."""
-    kept = prm.__dict__
-    return kept["made_for"] if kept.get("made_bytes") == bytes(prm) else {}
+def _planned(where, prm, *args):
+    """Make the call by its plan; False where the checks have to decide."""
+    plan = prm.__dict__.get("plan")
+    status = -1 if plan is None else _call(plan, *args)
+    if status > 0:
+        _check(where, status)
+    return status == 0
 
 
-def _same(name, t, prm, made, shape_fields, stride_field, dtype):
+def _call(*args):
+    global _call
+    _call = load_marshal().call
+    return _call(*args)
+
+
+def _same(name, t, prm, shape_fields, stride_field, dtype):
     """Check that a tensor is the one its parameters were made for."""
-    if isinstance(t, torch.Tensor) and made.get(name) == (t.shape, t.stride(), t.dtype):
-        return
     shape, strides = _dims(name, t)
     want = tuple(getattr(prm, f) for f in shape_fields)
     if shape != want:
@@ -147,7 +154,7 @@ def make_norm_rotate(Q, K, Qo, Ko, *, eps=1e-6, norm=True, rot=None,
     prm.norm, prm.eps = int(bool(norm)), float(eps)
     prm.rot = d if rot is None else int(rot)
     prm.pairing = _option("pairing", pairing, PAIRINGS)
-    return _made(prm, Q=Q, K=K, Qo=Qo, Ko=Ko)
+    return _made(prm, 0, "sparsepr_norm_rotate", Q, K, Qo, Ko)
 
 
 def sparsepr_norm_rotate(prm, Q, K, Qo, Ko, wq=None, wk=None, cos=None, sin=None, pos_q=None,
@@ -158,12 +165,14 @@ def sparsepr_norm_rotate(prm, Q, K, Qo, Ko, wq=None, wk=None, cos=None, sin=None
     pos_q, pos_k: [B, N] int32 table row of each token (None: token n takes row n); status:
     optional int32[4] device tensor.  Qo may be Q and Ko may be K.
     """
-    made = _made_for(prm)
-    _same("Q", Q, prm, made, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype_in)
-    _same("Qo", Qo, prm, made, ("B", "Hq", "Nq", "d"), "qo_strides", prm.dtype_out)
+    if _planned("sparsepr_norm_rotate", prm, Q, K, Qo, Ko, wq, wk, cos, sin, pos_q, pos_k, status,
+                stream):
+        return
+    _same("Q", Q, prm, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype_in)
+    _same("Qo", Qo, prm, ("B", "Hq", "Nq", "d"), "qo_strides", prm.dtype_out)
     if prm.Hk:
-        _same("K", K, prm, made, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype_in)
-        _same("Ko", Ko, prm, made, ("B", "Hk", "Nk", "d"), "ko_strides", prm.dtype_out)
+        _same("K", K, prm, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype_in)
+        _same("Ko", Ko, prm, ("B", "Hk", "Nk", "d"), "ko_strides", prm.dtype_out)
     elif K is not None or Ko is not None or wk is not None or pos_k is not None:
         raise ValueError("the parameters were made without keys")
     for name, w in (("wq", wq), ("wk", wk)):
@@ -212,7 +221,7 @@ def make_masked(Q, K, V, O, *, scale=0.0, softcap=0.0, causal=False,
     prm.scale, prm.softcap = float(scale), float(softcap)
     prm.causal = int(bool(causal))
     prm.q_start = ALIGN_END if q_start is None else int(q_start)
-    return _made(prm, Q=Q, K=K, V=V, O=O)
+    return _made(prm, 1, "sparsepr_attend_masked", Q, K, V, O)
 
 
 def sparsepr_attend_masked(prm, Q, K, V, O, ws, k_len=None, doc_q=None, doc_k=None, prefix=None,
@@ -224,11 +233,13 @@ def sparsepr_attend_masked(prm, Q, K, V, O, ws, k_len=None, doc_q=None, doc_k=No
     [Hq] fp32; lse: [B, Hq, Nq] fp32 output; status: optional int32[4].  Rows that see no key are
     zero (lse -inf).
     """
-    made = _made_for(prm)
-    _same("Q", Q, prm, made, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype)
-    _same("K", K, prm, made, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype)
-    _same("V", V, prm, made, ("B", "Hk", "Nk", "d"), "v_strides", prm.dtype)
-    _same("O", O, prm, made, ("B", "Hq", "Nq", "d"), "o_strides", prm.dtype)
+    if _planned("sparsepr_attend_masked", prm, Q, K, V, O, ws, k_len, doc_q, doc_k, prefix, slopes,
+                lse, status, stream):
+        return
+    _same("Q", Q, prm, ("B", "Hq", "Nq", "d"), "q_strides", prm.dtype)
+    _same("K", K, prm, ("B", "Hk", "Nk", "d"), "k_strides", prm.dtype)
+    _same("V", V, prm, ("B", "Hk", "Nk", "d"), "v_strides", prm.dtype)
+    _same("O", O, prm, ("B", "Hq", "Nq", "d"), "o_strides", prm.dtype)
     i32 = torch.int32
     for name, t in (("k_len", k_len), ("prefix", prefix)):
         if t is not None:
@@ -278,7 +289,7 @@ def make_project(X, W, Y, *, residual=None, act="none") -> SprProjectParams:
         if t.dtype != X.dtype:
             raise ValueError(f"{name} must be {X.dtype}, got {t.dtype}")
     prm.act = _option("act", act, ACTS)
-    return _made(prm, X=X, W=W, Y=Y, residual=r)
+    return _made(prm, 2, "sparsepr_project", X, W, Y, residual)
 
 
 def sparsepr_project(prm, X, W, Y, ws, bias=None, gate=None, residual=None, status=None,
@@ -288,15 +299,16 @@ def sparsepr_project(prm, X, W, Y, ws, bias=None, gate=None, residual=None, stat
     bias: [M]; gate: [B, M]; residual: Y's shape (may be Y itself); all of X's type.  status:
     optional int32[4].
     """
-    made = _made_for(prm)
-    _same("X", X, prm, made, ("B", "Hx", "N", "dx"), "x_strides", prm.dtype)
-    _same("Y", Y, prm, made, ("B", "Hy", "N", "dy"), "y_strides", prm.dtype)
+    if _planned("sparsepr_project", prm, X, W, Y, ws, bias, gate, residual, status, stream):
+        return
+    _same("X", X, prm, ("B", "Hx", "N", "dx"), "x_strides", prm.dtype)
+    _same("Y", Y, prm, ("B", "Hy", "N", "dy"), "y_strides", prm.dtype)
     M, K = prm.Hy * prm.dy, prm.Hx * prm.dx
     if not isinstance(W, torch.Tensor) or W.dtype != X.dtype or tuple(W.shape) != (M, K) or \
             (K > 1 and W.stride(1) != 1) or (M > 1 and W.stride(0) != prm.w_stride):
         raise ValueError("W must be the tensor its parameters were made with")
     if residual is not None:
-        _same("residual", residual, prm, made, ("B", "Hy", "N", "dy"), "r_strides", prm.dtype)
+        _same("residual", residual, prm, ("B", "Hy", "N", "dy"), "r_strides", prm.dtype)
     for name, t, shape in (("bias", bias, (M,)), ("gate", gate, (prm.B, M))):
         if t is not None:
             _aux(name, t, X.dtype, shape)
