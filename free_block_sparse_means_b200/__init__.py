@@ -12,12 +12,14 @@ from ._binding import (EXPORTS, LIB_PATH, PARTITION_RESPONSE, PARTITION_SEMANTIC
                        sparsepr_launch_count, sparsepr_partition, sparsepr_reconstruct,
                        sparsepr_route, sparsepr_version, sparsepr_workspace_size,
                        sparsepr_workspace_view, workspace_tensor)
+from .attention_block import AttentionBlock
 from .host_call import HostPipeline
 from .operators import (make_masked, make_norm_rotate, make_project, sparsepr_attend_masked,
                         sparsepr_norm_rotate, sparsepr_project)
 
 __all__ = [
-    "EXPORTS", "HostPipeline", "LIB_PATH", "PARTITION_RESPONSE", "PARTITION_SEMANTIC", "ROUTE_BUDGET", "ROUTE_TAU",
+    "AttentionBlock", "EXPORTS", "HostPipeline", "LIB_PATH", "PARTITION_RESPONSE",
+    "PARTITION_SEMANTIC", "ROUTE_BUDGET", "ROUTE_TAU",
     "VIEWS", "SparsePRError", "SprHeadStats", "SprMaskedParams", "SprNormRotateParams",
     "SprParams", "SprProjectParams", "alloc_workspace", "load_library", "make_masked",
     "make_norm_rotate", "make_params", "make_project", "sparsepr_attend",

@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         const int g = row / a.Nq, rep = a.Hq / a.Hk;
         qi = row - g * a.Nq;
         h = it.h0 + g;
-        live = g < a.pack && h < (it.h0 / rep + 1) * rep;
+        live = g < a.pack && h < (it.h0 / rep + 1) * rep && (SOLO || s == 0);
         if (!live) qi = 0, h = it.h0;
       }
       const int whole = it.lim.limit(it.q0 + (SOLO ? 0 : s * TBM));  // keys every row of the tile sees
@@ -1013,9 +1013,12 @@ Plan make_plan(const spr_masked_params& p, int sms) {
   // head, or of as many heads of the key head as fit.
   q.solo = p.Nq <= TBM;
   q.pack = q.solo && 2 * p.Nq <= TBM ? (rep < TBM / p.Nq ? rep : TBM / p.Nq) : 1;
+  q.ktiles = (p.Nk + TBN - 1) / TBN;
+  // ... which over up to three key tiles one stream of the other form takes, one
+  // after the other: a tile is 1.4 us, the join it saves 3.
+  if (q.ktiles <= 3) q.solo = false;
   q.ntile_h = p.Hk * ((rep + q.pack - 1) / q.pack);
   q.nqb = q.solo ? 1 : (p.Nq + 2 * TBM - 1) / (2 * TBM);
-  q.ktiles = (p.Nk + TBN - 1) / TBN;
   const int64_t tiles = (int64_t)p.B * q.ntile_h * q.nqb;
   // Key splits with the least estimated time, in cycles of an SM: a key tile
   // takes a SOLO block what its 4 d 128 bytes take at 24 bytes a cycle (the

@@ -32,6 +32,7 @@ struct NrArgs {
   int32_t* status;
   float eps, inv_d;
   int B, d, rot, halves, norm, table_rows, heads_per_group;
+  int joint;  // queries and keys have the same tokens and positions: one list of heads
 };
 
 // Eight channels as they lie in memory, and as fp32.
@@ -44,6 +45,17 @@ __device__ __forceinline__ Raw<T> fetch8(const T* p) {
   Raw<T> r;
 #pragma unroll
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+// The same for rows that are read once: they leave the L1 to the tables.
+template <typename T>
+__device__ __forceinline__ Raw<T> stream8(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.v[i].x), "=r"(r.v[i].y), "=r"(r.v[i].z), "=r"(r.v[i].w)
+                 : "l"(reinterpret_cast<const uint4*>(p) + i));
   return r;
 }
 __device__ __forceinline__ void widen(const Raw<bf16>& r, float* f) {
@@ -94,24 +106,36 @@ __device__ __forceinline__ void store8(float* p, const float* f) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Grid: x tiles of tokens, y groups of heads, z = batch and side.
+// Grid: x tiles of tokens, y groups of heads, z batch (and side, where they differ in tokens).
 template <typename TI, typename TO, int LPR>
 __global__ void __launch_bounds__(NR_THREADS) k_norm_rotate(const __grid_constant__ NrArgs a) {
-  const int b = blockIdx.z % a.B;
-  const NrSide& s = a.side[blockIdx.z / a.B];
-  const int h0 = blockIdx.y * a.heads_per_group, h1 = min(s.H, h0 + a.heads_per_group);
+  const int b = blockIdx.z % a.B, z = blockIdx.z / a.B;
+  const NrSide& s0 = a.side[z];
+  const int h0 = blockIdx.y * a.heads_per_group, h1 = h0 + a.heads_per_group;
   const int l = threadIdx.x % LPR, c0 = 8 * l;  // this lane's channels c0 .. c0 + 7
   const int n = blockIdx.x * (NR_THREADS / LPR) + threadIdx.x / LPR;
-  if (h0 >= s.H) return;
+  if (h0 >= s0.H + (a.joint ? a.side[1].H : 0)) return;
   // lanes without a row or channels stay for the shuffles
-  bool live = n < s.N;
+  bool live = n < s0.N;
   const bool mine = c0 < a.d;
+  // heads hb .. of side s: their rows are on the way while the angles are fetched
+  Raw<TI> raw[NR_HEADS];
+  auto fetch = [&](const NrSide& s, int hb, int hi) {
+    const TI* x = static_cast<const TI*>(s.x) + b * s.xs[0] + (int64_t)n * s.xs[2] + c0;
+#pragma unroll
+    for (int u = 0; u < NR_HEADS; ++u)
+      if (live && mine && hb + u < hi) raw[u] = stream8(x + (hb + u) * s.xs[1]);
+  };
+  // this group's heads of the queries, then of the keys
+  const int lo0 = h0, hi0 = min(h1, s0.H), lo1 = max(h0 - s0.H, 0), hi1 = a.joint ? min(h1 - s0.H, a.side[1].H) : 0;
+  const bool has0 = lo0 < hi0;
+  fetch(has0 ? s0 : a.side[1], has0 ? lo0 : lo1, has0 ? hi0 : hi1);
   float cs[8], sn[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
   const int half = a.rot >> 1;
   if (live && a.rot) {
-    const int row = s.pos ? s.pos[(int64_t)b * s.N + n] : n;
+    const int row = s0.pos ? s0.pos[(int64_t)b * s0.N + n] : n;
     if (row < 0 || row >= a.table_rows) {
       if (a.status && l == 0 && h0 == 0 && atomicCAS(a.status, 0, (int)ERR_INDEX) == 0) {
         a.status[1] = b;
@@ -133,53 +157,64 @@ __global__ void __launch_bounds__(NR_THREADS) k_norm_rotate(const __grid_constan
       }
     }
   }
-  float w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  if (s.w && mine) load8(static_cast<const TI*>(s.w) + c0, w);
   const bool turned = c0 < a.rot, low = c0 < half;
   const int partner = low ? (threadIdx.x & 31) + half / 8 : (threadIdx.x & 31) - half / 8;
-  const TI* x = static_cast<const TI*>(s.x) + b * s.xs[0] + (int64_t)n * s.xs[2] + c0;
-  TO* y = static_cast<TO*>(s.y) + b * s.ys[0] + (int64_t)n * s.ys[2] + c0;
-  for (int hb = h0; hb < h1; hb += NR_HEADS) {
-    Raw<TI> raw[NR_HEADS];
+  for (int part = has0 ? 0 : 1; part < 2; ++part) {
+    const NrSide& s = part ? a.side[1] : s0;
+    const int lo = part ? lo1 : lo0, hi = part ? hi1 : hi0;
+    if (lo >= hi) break;
+    // The weights go into the angles once for all heads: y_c = r (x_c cw_c + x_o sw_c) with
+    // o the other channel of the pair, r the row's reciprocal root.
+    float w[8], cw[8], sw[8];
 #pragma unroll
-    for (int u = 0; u < NR_HEADS; ++u)
-      if (live && mine && hb + u < h1) raw[u] = fetch8(x + (hb + u) * s.xs[1]);
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (s.w && mine) load8(static_cast<const TI*>(s.w) + c0, w);
 #pragma unroll
-    for (int u = 0; u < NR_HEADS; ++u) {
-      if (hb + u >= h1) break;  // the same for the whole block
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-      if (live && mine) widen(raw[u], f);
-      if (a.norm) {
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(f[i], f[i], q);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-        const float r = rsqrtf(fmaf(q, a.inv_d, a.eps));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+    for (int i = 0; i < 8; ++i) {
+      if (a.halves) {
+        const float wo = __shfl_sync(0xffffffffu, w[i], partner);
+        cw[i] = cs[i] * w[i];
+        sw[i] = (low ? -sn[i] : sn[i]) * wo;
+      } else {
+        cw[i] = cs[i >> 1] * w[i];
+        sw[i] = (i & 1 ? sn[i >> 1] : -sn[i >> 1]) * w[i ^ 1];
       }
-      if (a.rot) {
-        if (a.halves) {
+    }
+    TO* y = static_cast<TO*>(s.y) + b * s.ys[0] + (int64_t)n * s.ys[2] + c0;
+    for (int hb = lo; hb < hi; hb += NR_HEADS) {
+      if (hb > lo || (part && has0)) fetch(s, hb, hi);
+#pragma unroll
+      for (int u = 0; u < NR_HEADS; ++u) {
+        if (hb + u >= hi) break;  // the same for the whole block
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+        if (live && mine) widen(raw[u], f);
+        float r = 1.f;
+        if (a.norm) {
+          float q = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q = fmaf(f[i], f[i], q);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+          r = rsqrtf(fmaf(q, a.inv_d, a.eps));
+        }
+        if (a.halves && a.rot) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float o = __shfl_sync(0xffffffffu, f[i], partner);
-            if (turned) f[i] = low ? f[i] * cs[i] - o * sn[i] : o * sn[i] + f[i] * cs[i];
+            f[i] = turned ? fmaf(o, sw[i], f[i] * cw[i]) * r : f[i] * cw[i] * r;
           }
-        } else if (turned) {
+        } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float p = f[2 * i], q = f[2 * i + 1];
-            f[2 * i] = p * cs[i] - q * sn[i];
-            f[2 * i + 1] = p * sn[i] + q * cs[i];
+            f[2 * i] = turned ? fmaf(q, sw[2 * i], p * cw[2 * i]) * r : p * cw[2 * i] * r;
+            f[2 * i + 1] = turned ? fmaf(p, sw[2 * i + 1], q * cw[2 * i + 1]) * r : q * cw[2 * i + 1] * r;
           }
         }
+        if (live && mine) store8(y + (hb + u) * s.ys[1], f);
       }
-      if (live && mine) store8(y + (hb + u) * s.ys[1], f);
     }
   }
 }
@@ -189,17 +224,19 @@ cudaError_t launch(NrArgs a, cudaStream_t st) {
   const int lanes = a.d / 8;
   auto go = [&](auto kern, int lpr) {
     const int per = NR_THREADS / lpr;
-    const int N = max(a.side[0].N, a.side[1].H ? a.side[1].N : 0);
-    const int H = max(a.side[0].H, a.side[1].H);
-    // A thread takes its token's angles and weights once for a group of heads.
-    // Few tokens: one head per thread, so that the row is the only latency.
-    // Many: two rounds of NR_HEADS rows, as soon as that leaves eight blocks
-    // per SM, so that the tables are read an eighth as often as the rows.
-    const int64_t blocks = (int64_t)((N + per - 1) / per) * H * 2 * a.B;
-    const int64_t share = blocks / (8 * num_sms());
-    a.heads_per_group = share >= 2 * NR_HEADS ? 2 * NR_HEADS : share >= NR_HEADS ? NR_HEADS : 1;
+    const int sides = a.side[1].H && !a.joint ? 2 : 1;
+    const int N = sides == 2 ? max(a.side[0].N, a.side[1].N) : a.side[0].N;
+    const int H = a.joint ? a.side[0].H + a.side[1].H : max(a.side[0].H, a.side[1].H);
+    // A thread takes its token's angles once for a group of heads, NR_HEADS rows
+    // at a time; the fewer groups, the fewer times the tables are read.  As many
+    // groups as make eight blocks for every SM.
+    const int64_t blocks = (int64_t)((N + per - 1) / per) * sides * a.B;
+    const int most = (H + NR_HEADS - 1) / NR_HEADS;
+    const int64_t need = (8 * num_sms() + blocks - 1) / blocks;
+    const int groups = need < most ? (int)need : most;
+    a.heads_per_group = ((H + groups - 1) / groups + NR_HEADS - 1) / NR_HEADS * NR_HEADS;
     const dim3 grid((N + per - 1) / per, (H + a.heads_per_group - 1) / a.heads_per_group,
-                    (a.side[1].H ? 2 : 1) * a.B);
+                    sides * a.B);
     spr_launch(kern, grid, NR_THREADS, 0, st, a);
     return cudaGetLastError();
   };
@@ -283,6 +320,7 @@ extern "C" spr_status sparsepr_norm_rotate(const spr_norm_rotate_params* p, cons
   a.halves = p->pairing == SPR_PAIR_HALVES;
   a.norm = p->norm;
   a.table_rows = table_rows;
+  a.joint = keys && p->Nq == p->Nk && pos_q == pos_k;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (status && cudaMemsetAsync(status, 0, 4 * sizeof(int32_t), st) != cudaSuccess)
     return SPR_ECUDA;
