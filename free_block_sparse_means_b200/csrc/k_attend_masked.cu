@@ -63,6 +63,7 @@ struct AmArgs {
   const int32_t *k_len, *doc_q, *doc_k, *prefix;
   const float* slopes;
   int64_t os[3];
+  int o_wide;  // rows of O lie on 32 bytes
   int B, Hq, Hk, Nq, Nk, causal, q_start;
   int qmul_b, qmul_h, kmul_b, kmul_h, vmul_b, vmul_h;  // 0 where a TMA dimension has one entry
   float scale, softcap;
@@ -211,6 +212,11 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void store32(void* p, const uint32_t* u) {  // p on 32 bytes
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
@@ -221,28 +227,37 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Scores of a row, capped, in units of log 2: with z = x kz the score over the cap
-// (kz = scale / c), c tanh(z) = x scale (tanh(z) / z).  Where |z| <= 3/4 in all of
-// the tile's scores the quotient is a polynomial in z^2 (fitted for least error,
-// 2^-25 relative): 9 packed operations for two scores, none on the multi-function
-// unit.  False, with x spoiled, where a score lies beyond.
-__device__ __forceinline__ bool cap_near(float* x, float kz, float scale) {
+// The cap c tanh(x kz), kz = scale / c, of scores x, in units of log 2.  Where
+// |x kz| <= 0.6 in all of a tile's scores it is x times a polynomial in x^2: tanh(z) / z
+// fitted in z^2 for least error (2^-23.6 relative), with kz and the scale in its
+// coefficients; 6 packed operations for two scores, none on the multi-function unit.
+struct Cap {
+  float c0, c1, c2, c3, c4, most;  // coefficients, and the largest x^2 they hold for
+  __device__ __forceinline__ void init(float kz, float scale_log2) {
+    const float k2 = kz * kz;
+    c0 = scale_log2;
+    c1 = -0.33332622051239014f * k2 * c0;
+    c2 = 0.13313521444797516f * k2 * k2 * c0;
+    c3 = -0.05223110690712929f * k2 * k2 * k2 * c0;
+    c4 = 0.01564048044383526f * k2 * k2 * k2 * k2 * c0;
+    most = 0.36f / k2;
+  }
+};
+// False, with x spoiled, where a score lies beyond.
+__device__ __forceinline__ bool cap_near(float* x, const Cap& c) {
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
-    float z0, z1, u0, u1, p0, p1;
-    mul2(z0, z1, x[k], x[k + 1], kz, kz);
-    mul2(u0, u1, z0, z1, z0, z1);
+    float u0, u1, p0, p1;
+    mul2(u0, u1, x[k], x[k + 1], x[k], x[k + 1]);
     far[(k >> 1) & 3] = max3(far[(k >> 1) & 3], u0, u1);
-    fma2(p0, p1, u0, u1, -0.004789074882864952f, 0.019691824913024902f, 0.019691824913024902f);
-    fma2e(p0, p1, u0, u1, -0.053403016179800034f);
-    fma2e(p0, p1, u0, u1, 0.1332675963640213f);
-    fma2e(p0, p1, u0, u1, -0.33333081007003784f);
-    fma2e(p0, p1, u0, u1, 1.f);
-    mul2(x[k], x[k + 1], x[k], x[k + 1], scale, scale);
+    fma2(p0, p1, u0, u1, c.c4, c.c3);
+    fma2e(p0, p1, u0, u1, c.c2);
+    fma2e(p0, p1, u0, u1, c.c1);
+    fma2e(p0, p1, u0, u1, c.c0);
     mul2(x[k], x[k + 1], x[k], x[k + 1], p0, p1);
   }
-  const bool beyond = max3(fmaxf(far[0], far[1]), far[2], far[3]) > 0.5625f;
+  const bool beyond = max3(fmaxf(far[0], far[1]), far[2], far[3]) > c.most;
   return !__any_sync(0xffffffffu, beyond);
 }
 // The same for any scores: c tanh(z) = c - 2 c / (1 + e^(2 z)), zin = 2 kz log2 e and
@@ -256,13 +271,11 @@ __device__ __forceinline__ void cap_far(float* x, float zin, float cl) {
 __device__ __forceinline__ void bias_scores(float* x, float scale, float slope, float at) {
   if (__all_sync(0xffffffffu, at >= (float)(TBN - 1) || at <= 0.f)) {
     const float ns = at > 0.f ? -slope : slope;
-    float d0 = at, d1 = at - 1.f;
 #pragma unroll
     for (int k = 0; k < TBN; k += 2) {
       float y0, y1;
       mul2(y0, y1, x[k], x[k + 1], scale, scale);
-      fma2(x[k], x[k + 1], d0, d1, ns, y0, y1);
-      add2(d0, d1, -2.f, -2.f);
+      fma2(x[k], x[k + 1], at - (float)k, at - (float)(k + 1), ns, y0, y1);
     }
     return;
   }
@@ -272,7 +285,8 @@ __device__ __forceinline__ void bias_scores(float* x, float scale, float slope, 
 
 // Which of a tile's 128 keys a row sees (bit k of word k / 32): those below its
 // limit and, with documents, of its document.  The rows of a warp carry few
-// documents as a rule: one ballot per document and word serves all its rows.
+// documents as a rule: one ballot per document and word serves all its rows (lane l
+// holds the ids of keys l, 32 + l, 64 + l and 96 + l).
 __device__ __forceinline__ void seen_keys(uint32_t* seen, int left, bool docs, const int32_t* doc_k,
                                           int t0, int Nk, int docq) {
   const int lane = threadIdx.x & 31;
@@ -317,8 +331,9 @@ __device__ __forceinline__ float max_of(const float* x) {
 template <typename T>
 constexpr float p_shift() { return sizeof(T) == 2 && std::is_same<T, __half>::value ? 7.f : 0.f; }
 
-// XF: scores are capped or get the distance bias (both optional at run time).
-template <typename T, int D, bool SOLO, bool XF>
+// MODE: PLAIN scores, CAP tanh cap, BIAS distance penalty (and a cap, where given).
+enum { PLAIN, CAP, BIAS };
+template <typename T, int D, bool SOLO, int MODE>
 __global__ void __launch_bounds__(AM_THREADS, 1)
     k_attend_masked(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AmArgs a) {
@@ -579,6 +594,8 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     const uint32_t lane_f = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t scol = tbase + lane_f + s * 128, ocol = tbase + lane_f + O_COL + s * 128;
     const float scale_log2 = a.scale * LOG2E;
+    Cap cap;
+    if (MODE == CAP) cap.init(a.scale / a.softcap, scale_log2);
     int np = 0, no = 0, c = 0;  // tiles and items this stream has had, ring entries so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -597,7 +614,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       const int whole = it.lim.limit(it.q0 + (SOLO ? 0 : s * TBM));  // keys every row of the tile sees
       const int lim = live ? it.lim.limit(qi) : 0;
       const int docq = a.doc_q && live ? a.doc_q[(int64_t)it.b * a.Nq + qi] : 0;
-      const float slope = XF && a.slopes ? a.slopes[h] * LOG2E : 0.f;
+      const float slope = MODE == BIAS ? a.slopes[h] * LOG2E : 0.f;
       const int32_t* dk = a.doc_k ? a.doc_k + (int64_t)it.b * a.Nk : nullptr;
       const bool work = __any_sync(0xffffffffu, live);  // a warp without rows only keeps step
       float m = -INFINITY, l = 0.f;
@@ -628,26 +645,23 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         };
         auto take = [&]() {  // the row's scores, transformed and masked
           load();
-          if (XF) {
-            const bool cap = a.softcap > 0.f;
-            if (cap) {
-              const float kz = a.scale / a.softcap;
-              if (!far && !cap_near(x, kz, scale_log2)) {
-                far = true;  // for the rest of the item: such scores seldom come alone
-                load();
-              }
-              if (far) cap_far(x, 2.f * LOG2E * kz, a.softcap * LOG2E);
+          if (MODE != PLAIN && a.softcap > 0.f) {
+            if (MODE == CAP && !far && !cap_near(x, cap)) {
+              far = true;  // for the rest of the item: such scores seldom come alone
+              load();
             }
-            if (a.slopes || !cap)
-              bias_scores(x, cap ? 1.f : scale_log2, slope, (float)(it.lim.pos0 + qi - t0));
+            if (MODE == BIAS || far) cap_far(x, 2.f * LOG2E * a.scale / a.softcap, a.softcap * LOG2E);
           }
+          if (MODE == BIAS && a.slopes)  // (always: the branch keeps the loads from spilling)
+            bias_scores(x, a.softcap > 0.f ? 1.f : scale_log2, slope,
+                        (float)(it.lim.pos0 + qi - t0));
           if (part) {
 #pragma unroll
             for (int k = 0; k < TBN; ++k)
               if (!(seen[k / 32] & (1u << (k % 32)))) x[k] = -INFINITY;
           }
         };
-        const float sl2 = XF ? 1.f : scale_log2;
+        const float sl2 = MODE == PLAIN ? scale_log2 : 1.f;
         uint32_t pr[32];
         float sum4[4];
         // P of 64 keys from key K0 on.  A row that has seen nothing keeps m = -inf;
@@ -687,10 +701,10 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           }
           m = top;
         };
-        // XF: where every probability of the warp's rows would be flushed to 0 (a
+        // BIAS: where every probability of the warp's rows would be flushed to 0 (a
         // distance penalty far from the rows), there is no exponential to take.
         bool nothing = false;
-        if (XF) {
+        if (MODE == BIAS) {
           if (work) {
             take();
             const float mx = max_of(x);
@@ -786,8 +800,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             if (live) {
               uint4* d = reinterpret_cast<uint4*>(a.part_o + part * D + 32 * k);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                d[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) store32(d + 2 * e, o + 8 * e);
             }
           }
       } else {
@@ -808,15 +821,19 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
           if (live) {
+            uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t u[4];
+            for (int g = 0; g < 16; ++g)
+              u[g] = l == 0.f ? 0u
+                              : pack2<T>(__uint_as_float(o[2 * g]) * f,
+                                         __uint_as_float(o[2 * g + 1]) * f);
+            if (a.o_wide) {
+              store32(d + 4 * k, u);
+              store32(d + 4 * k + 2, u + 8);
+            } else {
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                u[g] = l == 0.f ? 0u
-                                : pack2<T>(__uint_as_float(o[8 * e + 2 * g]) * f,
-                                           __uint_as_float(o[8 * e + 2 * g + 1]) * f);
-              d[4 * k + e] = make_uint4(u[0], u[1], u[2], u[3]);
+              for (int e = 0; e < 4; ++e)
+                d[4 * k + e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
             }
           }
         }
@@ -1076,10 +1093,10 @@ bool make_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int B, in
   return encode_tmap(m, dt, 4, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename T, int D, bool SOLO, bool XF>
+template <typename T, int D, bool SOLO, int MODE>
 cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                    const CUtensorMap& v, int sms, cudaStream_t st) {
-  auto kern = k_attend_masked<T, D, SOLO, XF>;
+  auto kern = k_attend_masked<T, D, SOLO, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem_bytes<D>());
   if (e != cudaSuccess) return e;
@@ -1100,12 +1117,14 @@ cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
 template <typename T, int D>
 cudaError_t launch_for(bool solo, const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                        const CUtensorMap& v, int sms, cudaStream_t st) {
-  const bool xf = a.softcap > 0.f || a.slopes;
-  if (solo)
-    return xf ? launch<T, D, true, true>(a, q, k, v, sms, st)
-              : launch<T, D, true, false>(a, q, k, v, sms, st);
-  return xf ? launch<T, D, false, true>(a, q, k, v, sms, st)
-            : launch<T, D, false, false>(a, q, k, v, sms, st);
+  if (a.slopes)
+    return solo ? launch<T, D, true, BIAS>(a, q, k, v, sms, st)
+                : launch<T, D, false, BIAS>(a, q, k, v, sms, st);
+  if (a.softcap > 0.f)
+    return solo ? launch<T, D, true, CAP>(a, q, k, v, sms, st)
+                : launch<T, D, false, CAP>(a, q, k, v, sms, st);
+  return solo ? launch<T, D, true, PLAIN>(a, q, k, v, sms, st)
+              : launch<T, D, false, PLAIN>(a, q, k, v, sms, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -1176,6 +1195,7 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   a.prefix = prefix;
   a.slopes = slopes;
   for (int i = 0; i < 3; ++i) a.os[i] = p->o_strides[i];
+  a.o_wide = aligned(O, 32) && (a.os[0] | a.os[1] | a.os[2]) % 16 == 0;
   a.B = p->B;
   a.Hq = p->Hq;
   a.Hk = p->Hk;
