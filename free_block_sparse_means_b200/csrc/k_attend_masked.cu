@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tbase = *tmem_base_s;
+  after_previous();
 
   // Item k of this block, as a warp of the consumers sees it; false: no more.
   auto next_item = [&](int k, Item<SOLO>& it) {
@@ -867,6 +868,7 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
   __shared__ float sm[4], sl[4], so[4][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+  after_previous();
   const int64_t r = min((int64_t)blockIdx.x * ROWS + warp / WARPS, rows - 1);  // (batch, head, query)
   const int qi = (int)(r % a.Nq), h = (int)(r / a.Nq % a.Hq), b = (int)(r / a.Nq / a.Hq);
   const int rep = a.Hq / a.Hk, per = (rep + a.pack - 1) / a.pack;
@@ -937,6 +939,7 @@ __global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ A
   __shared__ int lo[2], hi[2], neg[2], final_entry[2], entry[32];
   const int b = blockIdx.y, blk = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int span = SOLO ? TBM : 2 * TBM, q0 = blk * span;
+  after_previous();
   if (threadIdx.x < 2) {
     lo[threadIdx.x] = INT32_MAX;
     hi[threadIdx.x] = -1;
@@ -1097,18 +1100,18 @@ template <typename T, int D, bool SOLO, int MODE>
 cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                    const CUtensorMap& v, int sms, cudaStream_t st) {
   auto kern = k_attend_masked<T, D, SOLO, MODE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem_bytes<D>());
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, smem_bytes<D>(), done);
   if (e != cudaSuccess) return e;
-  spr_launch(kern, a.n_items < sms ? a.n_items : sms, AM_THREADS, smem_bytes<D>(), st, q, k, v, a);
+  spr_launch_early(kern, a.n_items < sms ? a.n_items : sms, AM_THREADS, smem_bytes<D>(), st, q, k, v, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.partial) {
     const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
     // a warp goes through four parts in about 1 us; few rows with many parts get four warps each
     if ((SOLO ? 2 : 1) * a.nsplit > 8 && rows <= 65536)
-      spr_launch(k_am_join<T, D, SOLO, 4>, (unsigned)rows, 128, 0, st, a);
+      spr_launch_early(k_am_join<T, D, SOLO, 4>, (unsigned)rows, 128, 0, st, a);
     else
-      spr_launch(k_am_join<T, D, SOLO, 1>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
+      spr_launch_early(k_am_join<T, D, SOLO, 1>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
     e = cudaGetLastError();
   }
   return e;
@@ -1243,9 +1246,9 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   if (doc_q) {
     const dim3 grid(q.nqb, p->B);
     if (q.solo)
-      spr_launch(k_am_documents<true>, grid, 1024, 0, st, a, count, list);
+      spr_launch_early(k_am_documents<true>, grid, 1024, 0, st, a, count, list);
     else
-      spr_launch(k_am_documents<false>, grid, 1024, 0, st, a, count, list);
+      spr_launch_early(k_am_documents<false>, grid, 1024, 0, st, a, count, list);
     if (cudaGetLastError() != cudaSuccess) return SPR_ECUDA;
   }
   cudaError_t e;

@@ -109,6 +109,7 @@ __device__ __forceinline__ void store8(float* p, const float* f) {
 // Grid: x tiles of tokens, y groups of heads, z batch (and side, where they differ in tokens).
 template <typename TI, typename TO, int LPR>
 __global__ void __launch_bounds__(NR_THREADS) k_norm_rotate(const __grid_constant__ NrArgs a) {
+  after_previous();
   const int b = blockIdx.z % a.B, z = blockIdx.z / a.B;
   const NrSide& s0 = a.side[z];
   const int h0 = blockIdx.y * a.heads_per_group, h1 = h0 + a.heads_per_group;
@@ -237,7 +238,7 @@ cudaError_t launch(NrArgs a, cudaStream_t st) {
     a.heads_per_group = ((H + groups - 1) / groups + NR_HEADS - 1) / NR_HEADS * NR_HEADS;
     const dim3 grid((N + per - 1) / per, (H + a.heads_per_group - 1) / a.heads_per_group,
                     sides * a.B);
-    spr_launch(kern, grid, NR_THREADS, 0, st, a);
+    spr_launch_early(kern, grid, NR_THREADS, 0, st, a);
     return cudaGetLastError();
   };
   if (lanes > 16) return go(k_norm_rotate<TI, TO, 32>, 32);

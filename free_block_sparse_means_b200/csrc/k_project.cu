@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_project_few(const __grid_con
   __shared__ float sums[FEW_WARPS][8 * NG][OUT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int warps = blockDim.x >> 5;
+  after_previous();
   const int m0 = blockIdx.x * OUT, rows = a.B * a.N;
   const T* w[NT];
   bool has_w[NT];
@@ -318,6 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tbase = *tmem_base_s;
+  after_previous();
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
@@ -521,6 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
 // The splits' sums of 8 channels of a row, in their order, and the epilogue.
 template <typename T>
 __global__ void __launch_bounds__(256) k_project_join(const __grid_constant__ PjArgs a) {
+  after_previous();
   const int units = a.M / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)a.B * a.N * units) return;
@@ -664,14 +667,14 @@ bool make_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int B, in
 template <typename T>
 cudaError_t launch_pair(const PjArgs& a, const CUtensorMap& x, const CUtensorMap& w,
                         const CUtensorMap& y, const CUtensorMap& r, int sms, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(
-      k_project_pair<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PJ_SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_project_pair<T>, PJ_SMEM, done);
   if (e != cudaSuccess) return e;
   const int clusters = sms / 2 < a.n_items ? sms / 2 : a.n_items;
-  spr_launch(k_project_pair<T>, 2 * clusters, PJ_THREADS, PJ_SMEM, st, x, w, y, r, a);
+  spr_launch_early(k_project_pair<T>, 2 * clusters, PJ_THREADS, PJ_SMEM, st, x, w, y, r, a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.nsplit == 1) return e;
   const int64_t units = (int64_t)a.B * a.N * (a.M / 8);
-  spr_launch(k_project_join<T>, (unsigned)((units + 255) / 256), 256, 0, st, a);
+  spr_launch_early(k_project_join<T>, (unsigned)((units + 255) / 256), 256, 0, st, a);
   return cudaGetLastError();
 }
 
@@ -683,7 +686,7 @@ cudaError_t launch_few(const PjArgs& a, int sms, cudaStream_t st) {
   int warps = (22 * sms + blocks / 2) / blocks;
   if (warps > rounds) warps = rounds;
   warps = warps < 4 ? 4 : warps > FEW_WARPS ? FEW_WARPS : warps;
-  spr_launch(k_project_few<T, NG, NT, U>, blocks, 32 * warps, 0, st, a);
+  spr_launch_early(k_project_few<T, NG, NT, U>, blocks, 32 * warps, 0, st, a);
   return cudaGetLastError();
 }
 template <typename T>

@@ -2,6 +2,7 @@
 // public C ABI).  Workspace layout, launch helpers and device utilities.
 #pragma once
 
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -195,6 +196,35 @@ inline void spr_launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, 
   k<<<grid, block, smem, st>>>(args...);
   note_launch();
 }
+// The same for a kernel that begins with after_previous(): it may be set up on
+// the SMs while the kernel before it in the stream still runs.
+template <typename... KArgs, typename... Args>
+inline void spr_launch_early(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t st, Args... args) {
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = early;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, k, args...);
+  note_launch();
+}
+// Allow `kern` its shared memory, once per device (a call of the runtime each time otherwise).
+template <typename K>
+inline cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 #endif
 
 }  // namespace spr
@@ -227,6 +257,13 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// Wait until the kernels before this one in the stream have finished and their
+// writes are visible; then let the next one be set up.  Before the first access
+// to global memory, in every thread.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
