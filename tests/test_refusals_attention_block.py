@@ -52,3 +52,19 @@ def test_calls():
             (dense, (x, cos, cos), {})):  # the last: not on a GPU
         with pytest.raises(ValueError):
             block(*args, **kw)
+
+
+def test_strides_that_no_tensor_map_describes():
+    """One row for all tokens, or one query head for all heads, is refused; batches and key heads
+    may share."""
+    x, w, y = torch.zeros(2, 1, 40, 64, dtype=BF), torch.zeros(64, 64, dtype=BF), \
+        torch.zeros(2, 1, 40, 64, dtype=BF)
+    with pytest.raises(spr.SparsePRError):
+        spr.alloc_workspace(spr.make_project(x[:, :, :1].expand(2, 1, 40, 64), w, y), device="cpu")
+    assert spr.alloc_workspace(spr.make_project(x[:1].expand(2, 1, 40, 64), w, y),
+                               device="cpu").numel() > 0
+    q, k = torch.zeros(2, 4, 10, 64, dtype=BF), torch.zeros(2, 4, 30, 64, dtype=BF)
+    with pytest.raises(spr.SparsePRError):
+        spr.alloc_workspace(spr.make_masked(q[:, :1].expand(2, 4, 10, 64), k, k, q), device="cpu")
+    one = k[:1, :1].expand(2, 4, 30, 64)
+    assert spr.alloc_workspace(spr.make_masked(q, one, one, q), device="cpu").numel() > 0
