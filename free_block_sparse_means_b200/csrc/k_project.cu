@@ -418,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
       row_tile(a, rt, b, n);
       const int cols = min(a.bn, a.M - it.ct * a.bn);  // channels of the tile that exist
       const bool live_tile = rt < a.row_tiles;
+      const int rows = a.nb > 1 ? min(a.nb, a.B - b) * a.N : min(PBM, a.N - n);  // that exist
       // R of the next 64 channels from `c0` into this warpgroup's buffer, once Y has left it
       auto load_r = [&](int c0) {
         if (tid == 0) {
@@ -464,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
                                     a.M + col;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              if (c0 + 4 * j < cols)
+              if (c0 + 4 * j < cols && row < rows)
                 reinterpret_cast<uint4*>(p)[j] =
                     make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             continue;
@@ -627,10 +628,12 @@ size_t make_plan(const spr_project_params& p, int sms, PjArgs* a) {
   a->row_tiles = a->nb > 1 ? (a->B + a->nb - 1) / a->nb : a->B * a->tiles_per_batch;
   a->row_pairs = (a->row_tiles + 1) / 2;
   a->kchunks = (a->K + PBK - 1) / PBK;
-  // Channels of a tile and splits of K with the least estimated time, in cycles:
-  // a stage costs its products (2 bn) or its bytes from L2, 128 rows of X and
-  // bn / 2 of W at 64 bytes a cycle (256 + bn); a tile costs its start and
-  // drain; a split costs another launch, and the sums' way through L2.
+  // Channels of a tile and splits of K with the least estimated time, in cycles,
+  // from measured calls: a stage of 64 channels takes 200 + 1.7 bn (its products
+  // 2 bn; below 256 channels its bytes from L2), all weights at least what HBM
+  // takes for them; a tile costs 1,200 to change over; splits cost a second
+  // launch and the sums' way out and back.  64 rows x 2,048 x 2,048: bn 256 16.9 us,
+  // 192 14.8, 128 12.7, 128 in three splits 11.8; 700 rows: 18.0, 15.7, 14.0, 21.2.
   const int clusters = sms / 2;
   double best = 0;
   for (int bn = 256; bn >= 64; bn -= 64) {
@@ -640,8 +643,10 @@ size_t make_plan(const spr_project_params& p, int sms, PjArgs* a) {
       if (s > 1 && (tiles * s > clusters || a->kchunks < 4 * s)) break;
       const int64_t waves = (tiles * s + clusters - 1) / clusters;
       const int chunks = (a->kchunks + s - 1) / s;
-      const double cost = (double)waves * (chunks * (256.0 + bn) + 1200.0) + 1500.0 +
-                          (s > 1 ? 5000.0 + 2.0 * s * tiles * bn * 4 / 64 : 0.0);
+      const double stages = (double)waves * (chunks * (200.0 + 1.7 * bn) + 1200.0);
+      const double weights = 2.0 * a->M * a->K / 2100.0;
+      const double cost = (stages > weights ? stages : weights) +
+                          (s > 1 ? 7600.0 + 8.0 * s * a->B * a->N * a->M / 2600.0 : 0.0);
       if (best == 0 || cost < best) {
         best = cost;
         a->bn = bn;
