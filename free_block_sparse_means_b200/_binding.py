@@ -63,7 +63,14 @@ class SprHeadStats(ctypes.Structure):
     ]
 
 
-class SprNormRotateParams(ctypes.Structure):
+class _Planned(ctypes.Structure):
+    """Parameters that carry the plan of their calls; a copy has their fields, not the plan."""
+
+    def __reduce__(self):
+        return type(self).from_buffer_copy, (bytes(self),)
+
+
+class SprNormRotateParams(_Planned):
     _fields_ = [
         ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
         ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
@@ -75,7 +82,7 @@ class SprNormRotateParams(ctypes.Structure):
     ]
 
 
-class SprMaskedParams(ctypes.Structure):
+class SprMaskedParams(_Planned):
     _fields_ = [
         ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
         ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
@@ -86,7 +93,7 @@ class SprMaskedParams(ctypes.Structure):
     ]
 
 
-class SprProjectParams(ctypes.Structure):
+class SprProjectParams(_Planned):
     _fields_ = [
         ("B", ctypes.c_int32), ("N", ctypes.c_int32), ("Hx", ctypes.c_int32),
         ("dx", ctypes.c_int32), ("Hy", ctypes.c_int32), ("dy", ctypes.c_int32),

@@ -28,7 +28,7 @@ class AttentionBlock:
     sparse: a dict of make_params options selects the sparse call (bf16, as many key heads as query
     heads, no masks); otherwise the attention is dense with softcap, causal and slopes as given.
     cache: number of tokens the keys and values of earlier calls are kept for (dense only, causal by
-    position).
+    position), or another AttentionBlock to share the cache of (blocks for calls of other lengths).
     """
 
     def __init__(self, shape, heads, d, w_qkv, w_out, *, kv_heads=None, b_qkv=None, b_out=None,
@@ -41,6 +41,13 @@ class AttentionBlock:
         if tuple(w_qkv.shape) != ((heads + 2 * kv) * d, C):
             raise ValueError(f"w_qkv must have shape {((heads + 2 * kv) * d, C)}, got "
                              f"{tuple(w_qkv.shape)}")
+        shared = cache if isinstance(cache, AttentionBlock) else None
+        if shared is not None:
+            cache = shared.cache
+            if not cache or (shared.shape[0], shared.kv_heads, shared.d) != (B, kv, d) or \
+                    shared.keys.dtype != w_qkv.dtype or shared.keys.device != w_qkv.device:
+                raise ValueError("a shared cache must be one of the same batch, key heads, d, type "
+                                 "and device")
         if cache and cache < N:
             raise ValueError(f"a cache of {cache} tokens is too short for calls of {N}")
         if sparse is not None and w_qkv.dtype is not torch.bfloat16:
@@ -64,7 +71,8 @@ class AttentionBlock:
         self._w_own, self._w_v = w_qkv[:rows], w_qkv[rows:]
         self._p_in = make_project(x, self._w_own, self.qkv)
         if cache:
-            self.keys, self.values = empty(B, kv, cache, d), empty(B, kv, cache, d)
+            self.keys = shared.keys if shared else empty(B, kv, cache, d)
+            self.values = shared.values if shared else empty(B, kv, cache, d)
             self.k_len = torch.zeros(B, device=dev, dtype=torch.int32)
             k_to, v_to = self.keys[:, :, :N], self.values[:, :, :N]
             self._p_v = make_project(x, self._w_v, v_to)

@@ -32,8 +32,7 @@ struct Want {
 
 struct Plan {
   enum Kind { NORM_ROTATE, MASKED, PROJECT } kind;
-  const void* prm;             // the parameters' struct, which owns this plan
-  std::vector<uint8_t> bytes;  // what it held when the plan was made
+  std::vector<uint8_t> bytes;  // the parameters when the plan was made
   void* fn;                    // the library's entry point
   std::vector<Want> main;      // the tensors made for, in the order of the call
 };
@@ -65,8 +64,8 @@ PyObject* plan(PyObject*, PyObject* args) {
     return nullptr;
   auto p = std::make_unique<Plan>();
   p->kind = static_cast<Plan::Kind>(kind);
-  p->prm = reinterpret_cast<const void*>(prm);
-  p->bytes.assign(static_cast<const uint8_t*>(p->prm), static_cast<const uint8_t*>(p->prm) + size);
+  const auto* now = reinterpret_cast<const uint8_t*>(prm);
+  p->bytes.assign(now, now + size);
   p->fn = reinterpret_cast<void*>(fn);
   p->main.resize(PyTuple_GET_SIZE(tensors));
   for (size_t i = 0; i < p->main.size(); ++i)
@@ -116,17 +115,27 @@ struct Call {
   }
 };
 
-// call(plan, *tensors in the order of the Python function, stream): the library's
-// status, or -1 where the call is left to the Python checks.
+// call(plan, address of the parameters, *tensors in the order of the Python function,
+// stream): the library's status, or -1 where the call is left to the Python checks.
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  auto* p = n ? static_cast<Plan*>(PyCapsule_GetPointer(a[0], NAME)) : nullptr;
-  if (!p) return nullptr;
+  auto* p = n > 1 ? static_cast<Plan*>(PyCapsule_GetPointer(a[0], NAME)) : nullptr;
+  if (!p) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    return nullptr;
+  }
+  const void* now = PyLong_AsVoidPtr(a[1]);
+  if (!now) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "parameters without an address");
+    return nullptr;
+  }
+  ++a;  // a[1], a[2] .. are the tensors from here on
+  --n;
   const Py_ssize_t want = p->kind == Plan::NORM_ROTATE ? 13 : p->kind == Plan::MASKED ? 14 : 10;
   if (n != want) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
     return nullptr;
   }
-  if (a[n - 1] != Py_None || memcmp(p->bytes.data(), p->prm, p->bytes.size()))
+  if (a[n - 1] != Py_None || memcmp(p->bytes.data(), now, p->bytes.size()))
     return PyLong_FromLong(-1);
   Call c;
   const auto i32 = at::kInt;
@@ -136,7 +145,7 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   };
   auto here = [&] { return c.ok && c.device == static_cast<int>(c10::cuda::current_device()); };
   if (p->kind == Plan::NORM_ROTATE) {
-    const auto& m = *static_cast<const spr_norm_rotate_params*>(p->prm);
+    const auto& m = *static_cast<const spr_norm_rotate_params*>(now);
     void* t[4];
     for (int i = 0; i < 4; ++i) t[i] = c.main(a[1 + i], p->main[i]);
     if (!m.Hk && (a[6] != Py_None || a[10] != Py_None)) return PyLong_FromLong(-1);
@@ -162,7 +171,7 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
     status = reinterpret_cast<decltype(&sparsepr_norm_rotate)>(p->fn)(
         &m, t[0], t[1], wq, wk, cos, sin, (int32_t)rows, pq, pk, t[2], t[3], st, stream());
   } else if (p->kind == Plan::MASKED) {
-    const auto& m = *static_cast<const spr_masked_params*>(p->prm);
+    const auto& m = *static_cast<const spr_masked_params*>(now);
     void* t[4];
     for (int i = 0; i < 4; ++i) t[i] = c.main(a[1 + i], p->main[i]);
     const at::Tensor* ws = c.tensor(a[5]);
@@ -178,7 +187,7 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
         &m, t[0], t[1], t[2], k_len, doc_q, doc_k, prefix, slopes, t[3], lse, ws->data_ptr(),
         ws->nbytes(), st, stream());
   } else {
-    const auto& m = *static_cast<const spr_project_params*>(p->prm);
+    const auto& m = *static_cast<const spr_project_params*>(now);
     void* t[3];
     for (int i = 0; i < 3; ++i) t[i] = c.main(a[1 + i], p->main[i]);
     const at::Tensor* ws = c.tensor(a[4]);

@@ -61,7 +61,7 @@ def _made(prm, kind, where, *tensors):
 def _planned(where, prm, *args):
     """Make the call by its plan; False where the checks have to decide."""
     plan = prm.__dict__.get("plan")
-    status = -1 if plan is None else _call(plan, *args)
+    status = -1 if plan is None else _call(plan, ctypes.addressof(prm), *args)
     if status > 0:
         _check(where, status)
     return status == 0

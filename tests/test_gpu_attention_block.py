@@ -104,13 +104,12 @@ def test_prompt_frames_and_tokens_over_a_cache():
     W = weights(heads, kv, d, C, dt)
     cos, sin = tables(cache, d)
     x = randn((B, cache, C), dt, 9)
-    blocks = {n: spr.AttentionBlock((B, n, C), heads, d, kv_heads=kv, cache=cache, **W)
-              for n in (200, 150, 1)}
-    first = blocks[200]
+    first = spr.AttentionBlock((B, 200, C), heads, d, kv_heads=kv, cache=cache, **W)
+    blocks = {n: spr.AttentionBlock((B, n, C), heads, d, kv_heads=kv, cache=first, **W)
+              for n in (150, 1)}
+    blocks[200] = first
     first.keys.fill_(float("nan"))
     first.values.fill_(float("inf"))
-    for b in blocks.values():  # one cache for all lengths of a call
-        b.keys, b.values = first.keys, first.values
     at = 0
     for n in (200, 150, 150, 1, 1, 1):
         part = x[:, at:at + n].contiguous()

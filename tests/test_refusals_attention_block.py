@@ -1,4 +1,7 @@
 """What AttentionBlock refuses, on the CPU."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -28,6 +31,12 @@ def test_construction():
             spr.AttentionBlock((2, 10, 128), 4, 64, w, wo, **kw)
     with pytest.raises(ValueError):
         spr.AttentionBlock((2, 10, 128), 4, 64, w, wo[:, :192])
+    cached = spr.AttentionBlock((2, 10, 128), 4, 64, w, wo, cache=40)
+    plain = spr.AttentionBlock((2, 10, 128), 4, 64, w, wo)
+    assert spr.AttentionBlock((2, 1, 128), 4, 64, w, wo, cache=cached).keys is cached.keys
+    for shape, of in (((3, 10, 128), cached), ((2, 41, 128), cached), ((2, 10, 128), plain)):
+        with pytest.raises(ValueError):
+            spr.AttentionBlock(shape, 4, 64, w, wo, cache=of)
     with pytest.raises(ValueError):
         spr.AttentionBlock((2, 10, 128), 4, 64, w.half(), wo.half(), sparse=sparse)
     with pytest.raises(spr.SparsePRError):  # attention has no heads of 96 channels
@@ -68,3 +77,16 @@ def test_strides_that_no_tensor_map_describes():
         spr.alloc_workspace(spr.make_masked(q[:, :1].expand(2, 4, 10, 64), k, k, q), device="cpu")
     one = k[:1, :1].expand(2, 4, 30, 64)
     assert spr.alloc_workspace(spr.make_masked(q, one, one, q), device="cpu").numel() > 0
+
+
+def test_copied_parameters():
+    """A copy has the fields and outlives what it was made from."""
+    q = torch.zeros(2, 4, 10, 64, dtype=BF)
+    x, w = torch.zeros(2, 1, 10, 64, dtype=BF), torch.zeros(64, 64, dtype=BF)
+    for prm in (spr.make_masked(q, q, q, q, softcap=3.0), spr.make_norm_rotate(q, q, q, q),
+                spr.make_project(x, w, x)):
+        want = bytes(prm)
+        copies = [copy.copy(prm), copy.deepcopy(prm), pickle.loads(pickle.dumps(prm))]
+        del prm
+        for c in copies:
+            assert bytes(c) == want and "plan" not in c.__dict__
