@@ -81,7 +81,8 @@ struct AmArgs {
   int qmul_b, qmul_h, kmul_b, kmul_h, vmul_b, vmul_h;  // 0 where a TMA dimension has one entry
   float scale, softcap;
   // the plan: tiles of rows (heads packed per tile `pack`, query blocks `nqb`), key splits
-  int pack, ntile_h, nqb, nsplit, n_items, partial, by_block;
+  int pack, ntile_h, nqb, nsplit, n_items, by_block;
+  int n_tiles, n_whole;  // row tiles; the first n_whole are one item each, the rest nsplit
   // workspace: per row tile its listed key tiles (documents), partial results
   const int32_t *doc_count, *doc_list;
   int* next_item;  // counter of the items taken, or null: a fixed share for each block
@@ -115,14 +116,13 @@ struct Item {
   int nt[2];           // key tiles each stream visits, from key 0 on
   int last[2];         // entry after which a stream has no more tiles, at the latest
   int near;            // with a distance penalty: the tile of the rows' position, else -1
-  int64_t part;        // its first partial result
+  int64_t part;        // its first partial result, or -1: it writes O
   const int32_t* list; // documents: the listed tiles
   Limits lim;
-  __device__ void init(const AmArgs& a, int item) {
-    const int split = item % a.nsplit, at = item / a.nsplit, heads = a.B * a.ntile_h;
-    const int blk = a.by_block ? at / heads : at % a.nqb;
-    int t = a.by_block ? at % heads : at / a.nqb;
-    part = (int64_t)((t * a.nqb + blk) * a.nsplit + split) * 2;
+  // Row tile number `at`, in the order they are taken.
+  __device__ __forceinline__ void place(const AmArgs& a, int at) {
+    const int heads = a.B * a.ntile_h;
+    const int blk = a.by_block ? at / heads : at % a.nqb, t = a.by_block ? at % heads : at / a.nqb;
     const int ht = t % a.ntile_h;
     b = t / a.ntile_h;
     // heads: `pack` query heads per tile within a key head
@@ -131,6 +131,12 @@ struct Item {
     // blocks with the most keys first: later items then even out the SMs
     // (across all heads with by_block)
     q0 = (a.causal ? a.nqb - 1 - blk : blk) * (SOLO ? TBM : 2 * TBM);
+  }
+  __device__ void init(const AmArgs& a, int item) {
+    const bool whole = item < a.n_whole;
+    const int k = item - a.n_whole, ns = whole ? 1 : a.nsplit, split = whole ? 0 : k % ns;
+    part = whole ? -1 : (int64_t)k * 2;
+    place(a, whole ? item : a.n_whole + k / ns);
     lim.init(a, b);
     nt[0] = tiles(a, 0);
     nt[1] = SOLO ? nt[0] : tiles(a, 1);
@@ -146,7 +152,7 @@ struct Item {
       last[0] = a.doc_count[4 * row + 1];
       last[1] = a.doc_count[4 * row + 2];
     }
-    const int share = (most + a.nsplit - 1) / a.nsplit;
+    const int share = (most + ns - 1) / ns;
     i0 = min(most, split * share);
     n = min(most, i0 + share) - i0;
     for (int s = 0; s < 2; ++s) last[s] = SOLO ? n - 1 : min(last[s] - i0, n - 1);
@@ -735,10 +741,12 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           }
         } else {
           // the first half's exponentials go ahead with the maximum so far, under
-          // the search for the new one; they are seldom taken again
+          // the search for the new one; they are seldom taken again (the first
+          // tile's wait for its maximum)
           while (work) {
             take();
             const float mx = max_of(x) * sl2;
+            if (first) m = mx;
             sum4[0] = sum4[1] = sum4[2] = sum4[3] = 0.f;
             exps(Lo{});
             const bool grown = mx > m + 8.f;
@@ -798,7 +806,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         ++no;
         tc::tc_fence_after();
       }
-      if (a.partial) {
+      if (it.part >= 0) {
         const int64_t part = (it.part + s) * a.part_rows + row;
         if (live) {
           a.part_ml[2 * part] = m;
@@ -872,27 +880,32 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   }
 }
 
-// Add up the partial results of a row: a block per JOIN_ROWS rows, JOIN_WARPS
-// warps to a row, each with every JOIN_WARPS-th of the row's parts (2 nsplit of
-// them in the SOLO form, nsplit in the other), in an order that is fixed.
+// Add up the partial results of the rows of the split tiles: WARPS warps to a
+// row, each with every WARPS-th of the row's parts (2 nsplit of them in the SOLO
+// form, nsplit in the other), in an order that is fixed.
 template <typename T, int D, bool SOLO, int WARPS>
 __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs a) {
   constexpr int ROWS = 4 / WARPS, E = D / 32;
   __shared__ float sm[4], sl[4], so[4][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
   after_previous();
-  const int64_t r = min((int64_t)blockIdx.x * ROWS + warp / WARPS, rows - 1);  // (batch, head, query)
-  const int qi = (int)(r % a.Nq), h = (int)(r / a.Nq % a.Hq), b = (int)(r / a.Nq / a.Hq);
-  const int rep = a.Hq / a.Hk, per = (rep + a.pack - 1) / a.pack;
-  const int ht = h / rep * per + h % rep / a.pack;
-  const int span = SOLO ? TBM : 2 * TBM;
-  const int blk = a.causal ? a.nqb - 1 - qi / span : qi / span;
-  const int64_t tile = ((int64_t)b * a.ntile_h + ht) * a.nqb + blk;
-  const int s = SOLO ? 0 : qi % span / TBM;
-  const int row = a.pack > 1 ? h % rep % a.pack * a.Nq + qi : qi % TBM;
+  const int per_tile = SOLO ? a.part_rows : 2 * TBM;
+  const int64_t at = (int64_t)blockIdx.x * ROWS + warp / WARPS;
+  const int tt = (int)(at / per_tile), r = (int)(at % per_tile);  // split tile, its row
+  if (tt >= a.n_tiles - a.n_whole) return;
+  Item<SOLO> it;
+  it.place(a, a.n_whole + tt);
+  const int s = SOLO ? 0 : r / TBM, row = SOLO ? r : r % TBM, b = it.b;
+  int h = it.h0, qi = it.q0 + r;
+  if (a.pack > 1) {  // (SOLO)
+    const int rep = a.Hq / a.Hk;
+    h += row / a.Nq;
+    qi = row % a.Nq;
+    if (h >= (it.h0 / rep + 1) * rep) return;
+  }
+  if (qi >= a.Nq) return;
   const int np = SOLO ? 2 * a.nsplit : a.nsplit, step = SOLO ? 1 : 2;
-  const int64_t p0 = (tile * a.nsplit * 2 + s) * a.part_rows + row;
+  const int64_t p0 = ((int64_t)tt * a.nsplit * 2 + s) * a.part_rows + row;
   const int64_t pstep = (int64_t)step * a.part_rows;
   const int first = warp % WARPS;
   float M = -INFINITY;
@@ -902,13 +915,13 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
   float o[E] = {}, l = 0.f;
 #pragma unroll 4
   for (int p = first; p < np; p += WARPS) {
-    const int64_t at = p0 + p * pstep;
-    const float m = a.part_ml[2 * at], lp = a.part_ml[2 * at + 1];
+    const int64_t i = p0 + p * pstep;
+    const float m = a.part_ml[2 * i], lp = a.part_ml[2 * i + 1];
     if (lp == 0.f) continue;  // saw nothing; its O is not written
     const float w = ex2(m - M);
     l += w * lp;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, a.part_o[at * D + E * lane + e], o[e]);
+    for (int e = 0; e < E; ++e) o[e] = fmaf(w, a.part_o[i * D + E * lane + e], o[e]);
   }
   if (WARPS > 1) {
     if (lane == 0) sm[warp] = M, sl[warp] = l;
@@ -939,7 +952,8 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
   } else {
     *reinterpret_cast<uint32_t*>(O) = u0;
   }
-  if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -INFINITY : (M - p_shift<T>()) * LN2 + logf(l);
+  if (a.lse && lane == 0)
+    a.lse[((int64_t)b * a.Hq + h) * a.Nq + qi] = l == 0.f ? -INFINITY : (M - p_shift<T>()) * LN2 + logf(l);
 }
 
 // The key tiles that a row tile has to visit under documents: a block per (row
@@ -1035,7 +1049,7 @@ __global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ A
 // The plan of a call: which form, how many items, what the workspace holds.
 struct Plan {
   bool solo;
-  int pack, ntile_h, nqb, nsplit, n_items, ktiles, part_rows, by_block;
+  int pack, ntile_h, nqb, nsplit, n_items, ktiles, part_rows, by_block, n_tiles, n_whole;
   size_t next_off, count_off, list_off, o_off, ml_off, total;
 };
 
@@ -1055,10 +1069,10 @@ Plan make_plan(const spr_masked_params& p, int sms) {
   const int64_t tiles = (int64_t)p.B * q.ntile_h * q.nqb;
   // Key splits with the least estimated time, in cycles of an SM: a key tile
   // takes a SOLO block what its 4 d 128 bytes take at 24 bytes a cycle (the
-  // SM's share of HBM), the other form about 26 d cycles of softmax for its two
+  // SM's share of HBM), the other form about 3,300 cycles of softmax for its two
   // streams; an item costs 2,000 or 4,000 cycles to start and end; the join a launch and
   // the partial results' way out and back.  At least two tiles to a split.
-  const double step = q.solo ? 4.0 * p.d * TBN / 24 : 26.0 * p.d;
+  const double step = q.solo ? 4.0 * p.d * TBN / 24 : 3300.0;
   const double part = q.solo ? 2.0 * q.pack * p.Nq * p.d * 4 : 2.0 * TBM * p.d * 4;
   const int most = q.ktiles / 2 < 1 ? 1 : q.ktiles / 2;
   double best = 0;
@@ -1075,7 +1089,21 @@ Plan make_plan(const spr_masked_params& p, int sms) {
   // Causal items differ in length: heaviest first over all heads, as long as
   // the keys and values of all heads stay in L2 together.
   q.by_block = p.causal && !q.solo && 4.0 * p.B * p.Hk * p.Nk * p.d <= 48e6;
-  q.n_items = (int)(tiles * q.nsplit);
+  q.n_tiles = (int)tiles;
+  q.n_whole = q.solo || q.nsplit > 1 ? 0 : q.n_tiles;
+  // More tiles than SMs, of one length: those of a last round that leaves half
+  // of the SMs idle or more are split over them (24 heads x 8,192 x 8,192, 768 tiles on
+  // 148 SMs: 951 -> 854 us).
+  const int left = q.n_tiles % sms;
+  if (!p.causal && q.n_whole > sms && left && sms / left >= 2 && q.ktiles >= 4) {
+    const int n = sms / left < q.ktiles / 2 ? sms / left : q.ktiles / 2;
+    if (q.ktiles * step * (n - 1) / n > 25000.0) {
+      q.nsplit = n;
+      q.n_whole = q.n_tiles - left;
+    }
+  }
+  const int split_items = (q.n_tiles - q.n_whole) * q.nsplit;
+  q.n_items = q.n_whole + split_items;
   q.part_rows = q.solo ? q.pack * p.Nq : TBM;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1086,9 +1114,8 @@ Plan make_plan(const spr_masked_params& p, int sms) {
   q.next_off = take(4);
   q.count_off = take((size_t)p.B * q.nqb * 16);
   q.list_off = take((size_t)p.B * q.nqb * q.ktiles * 4);
-  const bool partial = q.solo || q.nsplit > 1;
-  q.o_off = take(partial ? (size_t)q.n_items * 2 * q.part_rows * p.d * 4 : 0);
-  q.ml_off = take(partial ? (size_t)q.n_items * 2 * q.part_rows * 8 : 0);
+  q.o_off = take((size_t)split_items * 2 * q.part_rows * p.d * 4);
+  q.ml_off = take((size_t)split_items * 2 * q.part_rows * 8);
   q.total = at;
   return q;
 }
@@ -1118,8 +1145,8 @@ cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
   if (e != cudaSuccess) return e;
   spr_launch_early(kern, a.n_items < sms ? a.n_items : sms, AM_THREADS, smem_bytes<D>(), st, q, k, v, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.partial) {
-    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+  if (a.n_whole < a.n_tiles) {
+    const int64_t rows = (int64_t)(a.n_tiles - a.n_whole) * (SOLO ? a.part_rows : 2 * TBM);
     // a warp goes through four parts in about 1 us; few rows with many parts get four warps each
     if ((SOLO ? 2 : 1) * a.nsplit > 8 && rows <= 65536)
       spr_launch_early(k_am_join<T, D, SOLO, 4>, (unsigned)rows, 128, 0, st, a);
@@ -1227,15 +1254,20 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   a.nsplit = q.nsplit;
   a.by_block = q.by_block;
   a.n_items = q.n_items;
-  a.partial = q.solo || q.nsplit > 1;
+  a.n_tiles = q.n_tiles;
+  a.n_whole = q.n_whole;
+  if (q.n_whole && (doc_q || k_len)) {  // tiles of different lengths: none is split
+    a.nsplit = 1;
+    a.n_items = a.n_whole = q.n_tiles;
+  }
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* count = reinterpret_cast<int32_t*>(base + q.count_off);
   int32_t* list = reinterpret_cast<int32_t*>(base + q.list_off);
   a.doc_count = count;
   // Items of very different length are taken as blocks come free: documents, and
   // lengths where each block has several items (the counter costs a memset).
-  const bool uneven = doc_q || (k_len && p->B > 1 && q.n_items > 2 * sms);
-  a.next_item = uneven && q.n_items > sms ? reinterpret_cast<int*>(base + q.next_off) : nullptr;
+  const bool uneven = doc_q || (k_len && p->B > 1 && a.n_items > 2 * sms);
+  a.next_item = uneven && a.n_items > sms ? reinterpret_cast<int*>(base + q.next_off) : nullptr;
   a.doc_list = list;
   a.ktiles = q.ktiles;
   a.part_o = reinterpret_cast<float*>(base + q.o_off);

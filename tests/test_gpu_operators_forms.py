@@ -36,6 +36,23 @@ def test_lengths_in_more_items_than_blocks():
         assert (O[2] == 0).all()
 
 
+@pytest.mark.parametrize("kw", [{}, dict(softcap=20.0), "slopes", "lens", "docs"], ids=str)
+def test_last_round_of_tiles_split(kw):
+    """160 row tiles: 148 blocks take one whole each, the other 12 are split (not where lengths or
+    documents make them differ)."""
+    Q, K, V = tensors(2, 80, 80, 200, 1300, 64, BF, seed=28)
+    if kw == "slopes":
+        kw = dict(slopes=torch.linspace(0, 0.3, 80, device="cuda"))
+    elif kw == "lens":
+        kw = dict(k_len=torch.tensor([1300, 700], dtype=torch.int32, device="cuda"))
+    elif kw == "docs":
+        kw = dict(doc_q=(torch.arange(200, device="cuda", dtype=torch.int32) // 70).repeat(2, 1),
+                  doc_k=(torch.arange(1300, device="cuda", dtype=torch.int32) // 500).repeat(2, 1))
+    a = compare(Q, K, V, **kw)
+    b, _ = run(Q, K, V, **kw)
+    assert torch.equal(a, b)
+
+
 def test_causal_heads_in_more_items_than_blocks():
     Q, K, V = tensors(2, 40, 8, 900, 900, 64, BF, seed=22)
     compare(Q, K, V, causal=True)
