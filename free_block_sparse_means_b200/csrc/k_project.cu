@@ -43,12 +43,28 @@ constexpr int FEW_ROWS = 16;
 constexpr int PBM = 128;                       // rows of a CTA's half of a tile
 constexpr int PBK = 64;                        // channels of a stage: one swizzled 128-byte row
 constexpr uint32_t PBOX = PBM * 128;           // 16 KB: 128 rows of 64 channels
-constexpr int NST = 6;                         // stages, each X box and W box
+constexpr int NST = 5;                         // stages, each X box and W box
 constexpr int PJ_THREADS = 384;
 constexpr uint32_t PJ_TMEM = 512;              // two accumulators of 256 columns
 constexpr uint64_t PJ_WAIT_NS = 2000000000ull;  // 2 s
-constexpr size_t PJ_SMEM = 1024 + (size_t)(2 * NST + 2) * PBOX + 256;
+constexpr size_t PJ_SMEM = 1024 + (size_t)(2 * NST + 4) * PBOX + 256;
 constexpr int MAX_SPLIT = 8;
+
+// Division of 0 <= n < 2^31 by a fixed 1 <= d <= 2^31: with 2^s >= d and m = floor(2^(31 + s) / d) + 1,
+// n m >> (31 + s) is exact, as m d - 2^(31 + s) <= d <= 2^s (Granlund and Montgomery).  A tile's
+// place takes ten divisions, which cost its epilogue as much as its arithmetic.
+struct FastDiv {
+  uint32_t d, m, s;
+  void set(uint32_t by) {
+    d = by;
+    s = 0;
+    while ((1ull << s) < by) ++s;
+    m = (uint32_t)((1ull << (31 + s)) / by + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((uint64_t)(uint32_t)n * m >> (31 + s));
+  }
+};
 
 struct PjArgs {
   const void *X, *W, *bias, *gate, *R;
@@ -58,6 +74,8 @@ struct PjArgs {
   int gate_rows;  // rows of a batch where the batches are taken as one (else 0)
   // the pair kernel's plan
   int bn, nb, row_tiles, tiles_per_batch, row_pairs, col_tiles, nsplit, kchunks, n_items;
+  int share;  // stages of a split
+  FastDiv by_split, by_group, by_last, by_batch, by_dx, by_dy;  // splits; tiles of a block of row pairs; rows of the last block ..
   uint32_t x_bytes, r_bytes;  // of one box
   int xmul_b, xmul_h, ymul_b, ymul_h, rmul_b, rmul_h;  // 0 where a TMA dimension has one entry
   float* part;
@@ -127,6 +145,22 @@ template <typename T>
 __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(pair_of<T>(f[0], f[1]), pair_of<T>(f[2], f[3]), pair_of<T>(f[4], f[5]),
                     pair_of<T>(f[6], f[7]));
+}
+// op(f, c) of 64 neighbouring channels from `col` on, c the row `p` of M values.  Channels
+// behind the last (of a ragged tile: clipped when it is stored) take some others' values.
+template <typename T, typename Op>
+__device__ __forceinline__ void each8(float* f, const T* p, int col, int M, Op op) {
+  uint4 c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    c[j] = __ldg(reinterpret_cast<const uint4*>(p + min(col + 8 * j, M - 8)));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float g[8];
+    unpack8<T>(c[j], g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[8 * j + i] = op(f[8 * j + i], g[i]);
+  }
 }
 // `f` with the activation as a compile-time constant
 template <typename F>
@@ -258,21 +292,21 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_project_few(const __grid_con
 // ------------------------------------------------------------ pairs of CTAs
 // Row tile t: its first batch and row.
 __device__ __forceinline__ void row_tile(const PjArgs& a, int t, int& b, int& n) {
-  b = a.nb > 1 ? t * a.nb : t / a.tiles_per_batch;
-  n = a.nb > 1 ? 0 : t % a.tiles_per_batch * PBM;
+  b = a.nb > 1 ? t * a.nb : a.by_batch.div(t);
+  n = a.nb > 1 ? 0 : (t - b * a.tiles_per_batch) * PBM;
 }
 // Item: blocks of 8 row pairs, channel tile by channel tile, so that the tiles
 // at work at one time share X and W in L2.
+constexpr int GROUP = 8;
 struct PjItem {
   int rp, ct, k0, k1, split;
   __device__ PjItem(const PjArgs& a, int item) {
-    constexpr int G = 8;
-    split = item % a.nsplit;
-    const int t = item / a.nsplit, group = t / (G * a.col_tiles), in = t % (G * a.col_tiles);
-    const int rows = min(G, a.row_pairs - group * G);
-    rp = group * G + in % rows;
-    ct = in / rows;
-    const int share = (a.kchunks + a.nsplit - 1) / a.nsplit;
+    const int t = a.by_split.div(item), group = a.by_group.div(t);
+    split = item - t * a.nsplit;
+    const int in = t - group * (GROUP * a.col_tiles), rows = min(GROUP, a.row_pairs - group * GROUP);
+    ct = rows == GROUP ? in / GROUP : a.by_last.div(in);
+    rp = group * GROUP + in - ct * rows;
+    const int share = a.share;
     k0 = min(split * share, a.kchunks);
     k1 = min(k0 + share, a.kchunks);
   }
@@ -288,8 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sX = base;
   uint8_t* sW = base + NST * PBOX;
-  uint8_t* sY = base + 2 * NST * PBOX;  // a buffer for each epilogue warpgroup
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + (2 * NST + 2) * PBOX);
+  uint8_t* sY = base + 2 * NST * PBOX;  // two buffers for each epilogue warpgroup
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + (2 * NST + 4) * PBOX);
   uint64_t* full = bars;                  // [NST] the first CTA's: both CTAs' loads
   uint64_t* empty = bars + NST;           // [NST]
   uint64_t* acc_full = bars + 2 * NST;    // [2]
@@ -340,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
         int b, n;
         row_tile(a, 2 * it.rp + rank, b, n);
         const int wrow = it.ct * a.bn + rank * (a.bn >> 1);
-        int h = it.k0 * PBK / a.dx, x = it.k0 * PBK - h * a.dx;
+        int h = a.by_dx.div(it.k0 * PBK), x = it.k0 * PBK - h * a.dx;
         for (int k = it.k0; k < it.k1; ++k, ++c) {
           const int s = c % NST;
           if (c >= NST &&
@@ -405,9 +439,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
     // ----------------------------------------------------------- epilogue
     const int wg = (warp - 4) >> 2, tid = threadIdx.x & 127, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    uint8_t* buf = sY + wg * PBOX;
+    // With a residual the first buffer is Y's and the second R's; without, Y takes
+    // them in turn.
+    uint8_t *const buf0 = sY + 2 * wg * PBOX, *const buf1 = buf0 + PBOX;
     const bool staged = a.nsplit == 1;
-    int t = 0, nr = 0;
+    int t = 0, nr = 0, ny = 0;
     // After a wait that gave up a warp still goes through its items, without
     // loading or storing sums, so that the warpgroup's barriers stay matched.
     bool ok = true, r_ok = true;
@@ -419,19 +455,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
       const int cols = min(a.bn, a.M - it.ct * a.bn);  // channels of the tile that exist
       const bool live_tile = rt < a.row_tiles;
       const int rows = a.nb > 1 ? min(a.nb, a.B - b) * a.N : min(PBM, a.N - n);  // that exist
-      // R of the next 64 channels from `c0` into this warpgroup's buffer, once Y has left it
+      // R of the 64 channels from `c0` on
       auto load_r = [&](int c0) {
-        if (tid == 0) {
-          tc::bulk_wait_read();
-          if (a.R && r_ok) {
-            const int col = it.ct * a.bn + c0, h = col / a.dy;
-            tc::mbar_expect_tx(r_full + wg, a.r_bytes);
-            tc::tma_load_4d(buf, &tmR, col - h * a.dy, n, h * a.rmul_h, b * a.rmul_b, r_full + wg);
-          }
+        if (tid == 0 && r_ok) {
+          const int col = it.ct * a.bn + c0, h = a.by_dy.div(col);
+          tc::mbar_expect_tx(r_full + wg, a.r_bytes);
+          tc::tma_load_4d(buf1, &tmR, col - h * a.dy, n, h * a.rmul_h, b * a.rmul_b, r_full + wg);
         }
       };
       const bool mine = live_tile && wg * 64 < cols;
-      if (staged && mine) load_r(wg * 64);
+      if (staged && mine && a.R) load_r(wg * 64);
       const bool any = it.k0 < it.k1;
       if (any && ok) {
         const bool got = tc::mbar_wait(acc_full + (t & 1), (t >> 1) & 1, abort_s, PJ_WAIT_NS);
@@ -440,6 +473,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
         tc::tc_fence_after();
       }
       const uint32_t acc = tbase + lanes + (t & 1) * 256;
+      auto release = [&]() {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(tc::leader_addr(acc_empty + (t & 1)));
+      };
       const T *bias = static_cast<const T*>(a.bias), *gate = static_cast<const T*>(a.gate);
       if (gate) {  // the row's batch
         int gb = b;
@@ -459,6 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 64; ++i) v[i] = 0u;
           }
+          if (any && c0 + 128 >= cols) release();  // the sums are in registers
           const int col = it.ct * a.bn + c0;
           if (!staged) {  // sums to the workspace
             float* p = a.part + ((int64_t)it.split * a.row_tiles * PBM + (int64_t)rt * PBM + row) *
@@ -470,7 +509,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
                     make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             continue;
           }
-          if (c0 > wg * 64) load_r(c0);
+          // the buffer's last store has left it
+          if (tid == 0) {
+            if (a.R)
+              tc::bulk_wait_read<0>();
+            else
+              tc::bulk_wait_read<1>();
+          }
           if (a.R) {
             // whatever became of the products, this load is in flight
             const bool got = r_ok && tc::mbar_wait_bounded(r_full + wg, nr & 1, PJ_WAIT_NS);
@@ -478,41 +523,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
             ++nr;
             r_ok = __all_sync(0xffffffffu, got);
             if (!r_ok) ok = false, *abort_s = 1;
-          } else {
-            tc::named_sync(1 + wg, 128);  // the buffer is free
           }
-          uint8_t* line = buf + row * 128;
-          with_act(a.act, [&](auto act) {
+          tc::named_sync(1 + wg, 128);
+          uint8_t* to = a.R || !(ny & 1) ? buf0 : buf1;
+          ++ny;
+          // Each step over all 64 channels: a branch for every 8 of them cost more than
+          // the arithmetic (1,650 cycles a chunk without any activation).
+          float* f = reinterpret_cast<float*>(v);
+          if (bias) each8<T>(f, bias, col, a.M, [](float x, float c) { return x + c; });
+          if (a.act != SPR_ACT_NONE)
+            with_act(a.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) f[i] = activate<decltype(act)::value>(f[i]);
+            });
+          if (gate) each8<T>(f, gate, col, a.M, [](float x, float c) { return x * c; });
+          if (a.R) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              float f[8];
+              float r[8];
+              unpack8<T>(*reinterpret_cast<const uint4*>(buf1 + row * 128 + ((j ^ (row & 7)) << 4)),
+                         r);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
-              const bool in = c0 + 8 * j < cols;
-              finish8<T, decltype(act)::value>(f, bias && in ? bias + col + 8 * j : nullptr,
-                                               gate && in ? gate + col + 8 * j : nullptr);
-              uint4* unit = reinterpret_cast<uint4*>(line + ((j ^ (row & 7)) << 4));
-              if (a.R) {
-                float r[8];
-                unpack8<T>(*unit, r);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] += r[i];
-              }
-              *unit = pack8<T>(f);
+              for (int i = 0; i < 8; ++i) f[8 * j + i] += r[i];
             }
-          });
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(to + row * 128 + ((j ^ (row & 7)) << 4)) = pack8<T>(f + 8 * j);
           tc::fence_proxy_async_smem();
           tc::named_sync(1 + wg, 128);
           if (tid == 0 && ok && !*abort_s) {
-            const int h = col / a.dy;
-            tc::tma_store_4d(&tmY, buf, col - h * a.dy, n, h * a.ymul_h, b * a.ymul_b);
+            const int h = a.by_dy.div(col);
+            tc::tma_store_4d(&tmY, to, col - h * a.dy, n, h * a.ymul_h, b * a.ymul_b);
             tc::bulk_commit();
           }
+          if (a.R && c0 + 128 < cols) load_r(c0 + 128);  // all threads have read this one's
         }
       if (any) {
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::leader_addr(acc_empty + (t & 1)));
+        if (!mine) release();
         ++t;
       }
     }
@@ -656,6 +704,13 @@ size_t make_plan(const spr_project_params& p, int sms, PjArgs* a) {
       }
     }
   }
+  a->share = (a->kchunks + a->nsplit - 1) / a->nsplit;
+  a->by_split.set(a->nsplit);
+  a->by_group.set(GROUP * a->col_tiles);
+  a->by_last.set(a->row_pairs % GROUP ? a->row_pairs % GROUP : GROUP);
+  a->by_batch.set(a->tiles_per_batch);
+  a->by_dx.set(a->dx);
+  a->by_dy.set(a->dy);
   return a->nsplit > 1 ? (size_t)a->nsplit * a->row_tiles * PBM * a->M * 4 : 256;
 }
 
