@@ -17,17 +17,18 @@
 //   the next.  Sharing W between the pair halves its traffic from L2, which a
 //   128 x 256 tile per CTA is bound by.
 //   A CTA: warp 0 loads into a ring of NST stages of 64 channels, warp 1 issues,
-//   warps 4-11 are the epilogue (two warpgroups, 64 channels in turn each).  The
-//   epilogue takes R by TMA into the buffer that Y then leaves from by TMA, which
-//   clips ragged edges and finds the head-major places.
+//   warps 4-11 are the epilogue (two warpgroups, 64 channels in turn each).  R comes
+//   and Y leaves by TMA, which clips ragged edges and finds the head-major places.
 //   Head-major X: 64 channels of K never cross a head (dx is a multiple of 64).
 //   Rows: a tile's 128 rows are of one batch, or of several whole batches of at
 //   most 64 rows (the box of the tensor map spans them).
 //   75,600 x 5,120 x 5,120 with gate and residual: 2.6 to 3.0 ms, 1,320 to 1,500
-//   TFLOP/s; the tensor pipe is busy 0.93 of the time and the clock is at 1.37 GHz, so
+//   TFLOP/s; the tensor pipe is busy 0.89 of the time and the clock is at 1.44 GHz, so
 //   the power limit is the bound.  8,190 x 2,048 x 6,144 (768 tiles on 74 pairs, 10.4
-//   rounds): 144 us, 1,430 TFLOP/s.  Under `lane == 0` instead of a uniform loop the
+//   rounds): 141 us, 1,460 TFLOP/s.  Under `lane == 0` instead of a uniform loop the
 //   issuing thread was the bound: 3,350 and 176 us.
+//   With few stages to a tile the epilogue is the bound: 65,144 x 344 x 4,360 with silu
+//   (two operations of the multi-function unit an output) 352 us, without 271.
 //   Where tiles are too few for the SMs, K is split, the sums go to the workspace
 //   in fp32 and k_project_join adds them and does the epilogue.
 //
@@ -75,7 +76,9 @@ struct PjArgs {
   // the pair kernel's plan
   int bn, nb, row_tiles, tiles_per_batch, row_pairs, col_tiles, nsplit, kchunks, n_items;
   int share;  // stages of a split
-  FastDiv by_split, by_group, by_last, by_batch, by_dx, by_dy;  // splits; tiles of a block of row pairs; rows of the last block ..
+  // by the splits, the tiles of a block of row pairs, the row pairs of the last block, a
+  // batch's row tiles, dx and dy
+  FastDiv by_split, by_group, by_last, by_batch, by_dx, by_dy;
   uint32_t x_bytes, r_bytes;  // of one box
   int xmul_b, xmul_h, ymul_b, ymul_h, rmul_b, rmul_h;  // 0 where a TMA dimension has one entry
   float* part;

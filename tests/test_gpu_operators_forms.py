@@ -237,3 +237,68 @@ def test_nan_in_a_row_stays_there():
     bad = ~torch.isfinite(out).all(-1)
     assert bad.nonzero().tolist() == [[0, 1, 7]]
     assert math.isfinite(out[0, 0].float().sum().item())
+
+
+# ------------------------------------------------- streams, together and captured
+def all_three(seed):
+    """A projection, a norm + rotation and an attention on tensors and workspaces of their own."""
+    x, w = randn((1, 1, 700, 512), BF, seed), randn((6 * 64, 512), BF, seed + 1, 0.05)
+    qkv = torch.empty(1, 6, 700, 64, device="cuda", dtype=BF)
+    q, k, v = qkv[:, :2], qkv[:, 2:4], qkv[:, 4:]
+    o = torch.empty(1, 2, 700, 64, device="cuda", dtype=BF)
+    cos = torch.ones(700, 32, device="cuda")
+    doc = (torch.arange(700, device="cuda", dtype=torch.int32) // 300).view(1, -1)
+    pj, nr, am = spr.make_project(x, w, qkv), spr.make_norm_rotate(q, k, q, k), \
+        spr.make_masked(q, k, v, o)
+    wp, wa = spr.alloc_workspace(pj), spr.alloc_workspace(am)
+
+    def call():
+        spr.sparsepr_project(pj, x, w, qkv, wp)
+        spr.sparsepr_norm_rotate(nr, q, k, q, k, cos=cos, sin=torch.zeros_like(cos))
+        spr.sparsepr_attend_masked(am, q, k, v, o, wa, doc_q=doc, doc_k=doc)
+    return call, o
+
+
+def test_two_streams_at_once():
+    calls = [all_three(41), all_three(43)]
+    want = []
+    for call, o in calls:
+        call()
+        want.append(o.clone())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for (call, o), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                o.zero_()
+                call()
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for (_, o), w in zip(calls, want):
+        assert torch.equal(o, w)
+
+
+def test_fork_and_join_in_a_capture():
+    """Two branches of one captured graph, joined, then both once more in a row."""
+    (a, oa), (b, ob) = all_three(45), all_three(47)
+    a(), b()
+    want = oa.clone(), ob.clone()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    total = torch.empty_like(oa)
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            b()
+        a()
+        here.wait_stream(side)
+        torch.add(oa, ob, out=total)
+        b()
+        a()
+    for _ in range(3):
+        oa.zero_(), ob.zero_(), total.zero_()
+        g.replay()
+        assert torch.equal(oa, want[0]) and torch.equal(ob, want[1])
+        assert torch.equal(total, want[0] + want[1])
