@@ -317,7 +317,7 @@ __device__ __forceinline__ void seen_keys(uint32_t* seen, int left, bool docs, c
   if (!docs) return;
   int id[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) id[k] = __ldg(doc_k + min(t0 + 32 * k + lane, Nk - 1));
+  for (int k = 0; k < 4; ++k) id[k] = doc_k[min(t0 + 32 * k + lane, Nk - 1)];
   uint32_t todo = __ballot_sync(0xffffffffu, left > 0 && docq >= 0);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
   while (todo) {

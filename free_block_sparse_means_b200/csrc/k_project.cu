@@ -131,7 +131,7 @@ template <typename T, int ACT>
 __device__ __forceinline__ void finish8(float* f, const T* bias, const T* gate) {
   if (bias) {
     float c[8];
-    unpack8<T>(__ldg(reinterpret_cast<const uint4*>(bias)), c);
+    unpack8<T>(*reinterpret_cast<const uint4*>(bias), c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] += c[i];
   }
@@ -139,7 +139,7 @@ __device__ __forceinline__ void finish8(float* f, const T* bias, const T* gate) 
   for (int i = 0; i < 8; ++i) f[i] = activate<ACT>(f[i]);
   if (gate) {
     float c[8];
-    unpack8<T>(__ldg(reinterpret_cast<const uint4*>(gate)), c);
+    unpack8<T>(*reinterpret_cast<const uint4*>(gate), c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] *= c[i];
   }
@@ -156,7 +156,7 @@ __device__ __forceinline__ void each8(float* f, const T* p, int col, int M, Op o
   uint4 c[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    c[j] = __ldg(reinterpret_cast<const uint4*>(p + min(col + 8 * j, M - 8)));
+    c[j] = *reinterpret_cast<const uint4*>(p + min(col + 8 * j, M - 8));
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float g[8];
@@ -179,9 +179,11 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // ------------------------------------------------------------------ few rows
+// Not through the read-only path (.nc): the kernel is resident before the one that may have
+// written the weights ends.
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_project_few(const __grid_con
         }
 #pragma unroll
       for (int i = 0; i < NG; ++i)
-        xv[u][i] = in && has_x[i] ? __ldg(reinterpret_cast<const uint4*>(x[i] + head + kx)) : zero;
+        xv[u][i] = in && has_x[i] ? *reinterpret_cast<const uint4*>(x[i] + head + kx) : zero;
       k += 32 * warps;
       kx += 32 * warps;
     }

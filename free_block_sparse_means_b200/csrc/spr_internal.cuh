@@ -261,7 +261,9 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // Wait until the kernels before this one in the stream have finished and their
 // writes are visible; then let the next one be set up.  Before the first access
-// to global memory, in every thread.
+// to global memory, in every thread.  Such a kernel reads by ordinary loads alone:
+// the read-only path (__ldg, ld.global.nc) is for data that nothing writes while the
+// kernel is resident, and the compiler need not keep its loads behind this wait.
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;\n" ::: "memory");
 }
