@@ -1,8 +1,10 @@
 // The host side of the operators' calls in one step: the checks of operators.py
 // that pass for the tensors the parameters were made for, and the call of the
 // library's entry point.  Anything else (other tensors, another device, a
-// gradient, an explicit stream) is left to the Python checks, which either take
-// the call or say what is wrong with it; so this file raises no error of its own.
+// gradient, an explicit stream, a tensor without storage of its own, whose
+// accessors throw) is left to the Python checks, which either take the call or say
+// what is wrong with it; so this file raises no error of its own, and no C++
+// exception leaves it: that would end the process.
 //
 // A call of an operator on a few rows lasts 2 to 5 us on the GPU; the Python
 // checks and ctypes take 12 us on the host, this about 1.
@@ -55,7 +57,7 @@ bool to_want(PyObject* o, Want* w) {
 }
 
 // plan(kind, address of the parameters, their size, address of the entry point, tensors made for)
-PyObject* plan(PyObject*, PyObject* args) {
+PyObject* make_plan(PyObject* args) {
   int kind;
   unsigned long long prm, fn;
   Py_ssize_t size;
@@ -117,7 +119,7 @@ struct Call {
 
 // call(plan, address of the parameters, *tensors in the order of the Python function,
 // stream): the library's status, or -1 where the call is left to the Python checks.
-PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* make_call(PyObject* const* a, Py_ssize_t n) {
   auto* p = n > 1 ? static_cast<Plan*>(PyCapsule_GetPointer(a[0], NAME)) : nullptr;
   if (!p) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
@@ -201,6 +203,23 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
         &m, t[0], t[1], bias, gate, res, t[2], ws->data_ptr(), ws->nbytes(), st, stream());
   }
   return PyLong_FromLong(status);
+}
+
+// What `f` returns, or `otherwise` where it throws.
+template <typename F>
+PyObject* guarded(F&& f, PyObject* (*otherwise)()) {
+  try {
+    return f();
+  } catch (...) {
+    PyErr_Clear();
+    return otherwise();
+  }
+}
+PyObject* plan(PyObject*, PyObject* args) {
+  return guarded([&] { return make_plan(args); }, []() -> PyObject* { Py_RETURN_NONE; });
+}
+PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&] { return make_call(a, n); }, [] { return PyLong_FromLong(-1); });
 }
 
 PyMethodDef METHODS[] = {
