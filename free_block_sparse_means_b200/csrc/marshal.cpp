@@ -83,7 +83,8 @@ struct Call {
   const at::Tensor* tensor(PyObject* o) {
     if (!THPVariable_CheckExact(o)) return fail();
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || (grad && t.requires_grad())) return fail();
+    // (a tangent counts under no_grad too: only reverse mode is off there)
+    if (!t.is_cuda() || (grad && t.requires_grad()) || t._fw_grad(0).defined()) return fail();
     const int d = t.get_device();
     if (device < 0) device = d;
     return d == device ? &t : fail();

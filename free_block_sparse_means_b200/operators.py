@@ -4,13 +4,14 @@ Argument checks and marshalling only; the contract of each is in
 include/sparsepr.h.  Every function takes its output tensors from the caller,
 enqueues on `stream` (default: the current stream of the tensors' device) and
 returns without waiting.  They are forward only: a call whose inputs require a
-gradient while gradients are enabled is refused.
+gradient while gradients are enabled, or carry a forward-mode tangent, is refused.
 """
 from __future__ import annotations
 
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from ._binding import (SprMaskedParams, SprNormRotateParams, SprProjectParams, _check,
                        load_library, load_marshal)
@@ -104,12 +105,15 @@ def _run(where, tensors, names, stream, call, *args):
     """Check where the tensors live (the first one decides) and make the call there."""
     index = tensors[0].get_device()
     grad = torch.is_grad_enabled()
+    dual = forward_ad._current_level >= 0
     astray = None
     for i, t in enumerate(tensors):
         if t is not None:
             if grad and t.requires_grad:
                 raise ValueError(f"{where} has no backward pass; {names.split()[i]} requires a "
                                  "gradient (call it under torch.no_grad())")
+            if dual and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{where} has no derivative; {names.split()[i]} carries a tangent")
             if t.get_device() != index:
                 astray = i
     if index < 0 or astray is not None:
