@@ -106,6 +106,10 @@ struct Call {
     }
     return t->data_ptr();
   }
+  const at::Tensor* workspace(PyObject* o) {
+    const at::Tensor* t = tensor(o);
+    return t && t->is_contiguous() ? t : fail();
+  }
   void* aux(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> sizes) {
     if (o == Py_None) return nullptr;
     const at::Tensor* t = tensor(o);
@@ -177,7 +181,7 @@ PyObject* make_call(PyObject* const* a, Py_ssize_t n) {
     const auto& m = *static_cast<const spr_masked_params*>(now);
     void* t[4];
     for (int i = 0; i < 4; ++i) t[i] = c.main(a[1 + i], p->main[i]);
-    const at::Tensor* ws = c.tensor(a[5]);
+    const at::Tensor* ws = c.workspace(a[5]);
     auto* k_len = static_cast<int32_t*>(c.aux(a[6], i32, {m.B}));
     auto* doc_q = static_cast<int32_t*>(c.aux(a[7], i32, {m.B, m.Nq}));
     auto* doc_k = static_cast<int32_t*>(c.aux(a[8], i32, {m.B, m.Nk}));
@@ -193,7 +197,7 @@ PyObject* make_call(PyObject* const* a, Py_ssize_t n) {
     const auto& m = *static_cast<const spr_project_params*>(now);
     void* t[3];
     for (int i = 0; i < 3; ++i) t[i] = c.main(a[1 + i], p->main[i]);
-    const at::Tensor* ws = c.tensor(a[4]);
+    const at::Tensor* ws = c.workspace(a[4]);
     const auto type = p->main[0].type;
     const int64_t M = (int64_t)m.Hy * m.dy;
     void *bias = c.aux(a[5], type, {M}), *gate = c.aux(a[6], type, {m.B, M});

@@ -97,6 +97,14 @@ def _aux(name, t, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace(ws):
+    """A workspace is as large as its elements say only where they lie one after the other."""
+    if not isinstance(ws, torch.Tensor):
+        raise ValueError("ws must be a torch tensor")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -258,6 +266,7 @@ def sparsepr_attend_masked(prm, Q, K, V, O, ws, k_len=None, doc_q=None, doc_k=No
         _aux("lse", lse, torch.float32, (prm.B, prm.Hq, prm.Nq))
     if status is not None:
         _aux("status", status, i32, (4,))
+    _workspace(ws)
     if (doc_q is None) != (doc_k is None):
         raise ValueError("doc_q and doc_k go together")
     if prefix is not None and not prm.causal:
@@ -313,6 +322,7 @@ def sparsepr_project(prm, X, W, Y, ws, bias=None, gate=None, residual=None, stat
         raise ValueError("W must be the tensor its parameters were made with")
     if residual is not None:
         _same("residual", residual, prm, ("B", "Hy", "N", "dy"), "r_strides", prm.dtype)
+    _workspace(ws)
     for name, t, shape in (("bias", bias, (M,)), ("gate", gate, (prm.B, M))):
         if t is not None:
             _aux(name, t, X.dtype, shape)
