@@ -294,6 +294,9 @@ extern "C" spr_status sparsepr_norm_rotate(const spr_norm_rotate_params* p, cons
     if (!aligned(cos, 16) || !aligned(sin, 16)) return SPR_EUNSUPPORTED;
   }
   if (p->B > 32767 || p->Hq > 65535 || p->Hk > 65535) return SPR_EUNSUPPORTED;
+  // (the last block's threads number tokens past the last)
+  if (p->Nq > INT32_MAX - NR_THREADS || (keys && p->Nk > INT32_MAX - NR_THREADS))
+    return SPR_EUNSUPPORTED;
   const int nq[3] = {p->B, p->Hq, p->Nq}, nk[3] = {p->B, p->Hk, p->Nk};
   const int pi = p->dtype_in == SPR_FP32 ? 4 : 8, po = p->dtype_out == SPR_FP32 ? 4 : 8;
   if (!side_strides_ok(p->q_strides, nq, pi, false) || !side_strides_ok(p->qo_strides, nq, po, true))

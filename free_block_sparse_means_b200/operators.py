@@ -20,6 +20,7 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 PAIRINGS = {"interleaved": 0, "halves": 1}
 ACTS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 ALIGN_END = -2 ** 31
+INT32_MAX = 2 ** 31 - 1
 
 
 def _dims(name, t):
@@ -29,6 +30,8 @@ def _dims(name, t):
         raise ValueError(f"{name} must be a torch tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be a 4-dimensional tensor, got {tuple(t.shape)}")
+    if max(t.shape) > INT32_MAX:
+        raise ValueError(f"{name} has more than 2^31 - 1 entries in a dimension: {tuple(t.shape)}")
     B, H, N, d = t.shape
     if d > 1 and t.stride(3) != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
@@ -48,6 +51,14 @@ def _option(name, value, table):
     if value not in table:
         raise ValueError(f"{name} must be one of {sorted(table)}, not {value!r}")
     return table[value]
+
+
+def _single(name, value):
+    """A number for a field whose 0 has a meaning of its own: one that fp32 rounds to 0 is refused."""
+    value = float(value)
+    if value and not ctypes.c_float(value).value:
+        raise ValueError(f"{name} = {value} is 0 in fp32")
+    return value
 
 
 def _made(prm, kind, where, *tensors):
@@ -165,6 +176,8 @@ def make_norm_rotate(Q, K, Qo, Ko, *, eps=1e-6, norm=True, rot=None,
         prm.Hk, prm.Nk = shape[1], shape[2]
     prm.norm, prm.eps = int(bool(norm)), float(eps)
     prm.rot = d if rot is None else int(rot)
+    if rot is not None and not 0 <= int(rot) <= d:
+        raise ValueError(f"rot must be 0..{d}, got {rot}")
     prm.pairing = _option("pairing", pairing, PAIRINGS)
     return _made(prm, 0, "sparsepr_norm_rotate", Q, K, Qo, Ko)
 
@@ -230,8 +243,10 @@ def make_masked(Q, K, V, O, *, scale=0.0, softcap=0.0, causal=False,
     for name, t in (("K", K), ("V", V), ("O", O)):
         if t.dtype != Q.dtype:
             raise ValueError(f"{name} must be {Q.dtype}, got {t.dtype}")
-    prm.scale, prm.softcap = float(scale), float(softcap)
+    prm.scale, prm.softcap = _single("scale", scale), _single("softcap", softcap)
     prm.causal = int(bool(causal))
+    if q_start is not None and abs(int(q_start)) > 1 << 30:
+        raise ValueError(f"q_start must be -2^30..2^30, got {q_start}")
     prm.q_start = ALIGN_END if q_start is None else int(q_start)
     return _made(prm, 1, "sparsepr_attend_masked", Q, K, V, O)
 
