@@ -84,8 +84,10 @@ class AttentionBlock:
         if sparse is not None:
             self._attend = spr.make_params(self.q, self.keys, self.values, self.o, **sparse)
         else:
+            # token n sits at position n, also in a batch of which only k_len tokens are real; with
+            # a cache the call's tokens are its last ones
             self._attend = make_masked(self.q, self.keys, self.values, self.o, softcap=softcap,
-                                       causal=causal or bool(cache))
+                                       causal=causal or bool(cache), q_start=None if cache else 0)
         self._p_out = make_project(self.o, w_out, y, residual=x)
         # the steps of a call follow one another, so one workspace serves them all but the sparse
         # call, which may keep centroids in its own for the next call
@@ -102,7 +104,8 @@ class AttentionBlock:
         cos, sin: tables of the rotation; positions: [B, N] table rows (default: token n takes row
         n, with a cache row at + n); at: number of tokens already in the cache; gate: [B, C];
         k_len, prefix: [B] and doc: [B, N], the masks of sparsepr_attend_masked (k_len and doc not
-        with a cache).
+        with a cache).  Token n is at position n, with a cache at + n, for the causal mask and the
+        slopes.  The tokens of a frame see one another and all before them with prefix = at + N.
         """
         B, N, C = self.shape
         if tuple(x.shape) != self.shape or not x.is_contiguous():
