@@ -262,8 +262,9 @@ struct Cap {
     most = 0.36f / k2;
   }
 };
-// False, with x spoiled, where a score lies beyond.
-__device__ __forceinline__ bool cap_near(float* x, const Cap& c) {
+// False, with x spoiled, where a score lies beyond.  Rows that are not `live` have no say:
+// theirs come of whatever the shared memory behind packed rows held.
+__device__ __forceinline__ bool cap_near(float* x, const Cap& c, bool live) {
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
@@ -276,7 +277,7 @@ __device__ __forceinline__ bool cap_near(float* x, const Cap& c) {
     fma2e(p0, p1, u0, u1, c.c0);
     mul2(x[k], x[k + 1], x[k], x[k + 1], p0, p1);
   }
-  const bool beyond = max3(fmaxf(far[0], far[1]), far[2], far[3]) > c.most;
+  const bool beyond = live && max3(fmaxf(far[0], far[1]), far[2], far[3]) > c.most;
   return !__any_sync(0xffffffffu, beyond);
 }
 // The same for any scores: c tanh(z) = c - 2 c / (1 + e^(2 z)), zin = 2 kz log2 e and
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         auto take = [&]() {  // the row's scores, transformed and masked
           load();
           if (MODE != PLAIN && a.softcap > 0.f) {
-            if (MODE == CAP && !far && !cap_near(x, cap)) {
+            if (MODE == CAP && !far && !cap_near(x, cap, live)) {
               far = true;  // for the rest of the item: such scores seldom come alone
               load();
             }
@@ -728,9 +729,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           if (work) {
             take();
             const float mx = max_of(x);
-            const bool grown = mx > m + 8.f;
+            const bool grown = live && mx > m + 8.f;
             if (__any_sync(0xffffffffu, grown)) move_max(grown, mx);
-            nothing = __all_sync(0xffffffffu, mx < m - 140.f);
+            nothing = __all_sync(0xffffffffu, !live || mx < m - 140.f);
             sum4[0] = sum4[1] = sum4[2] = sum4[3] = 0.f;
             if (nothing) {
 #pragma unroll
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             if (first) m = mx;
             sum4[0] = sum4[1] = sum4[2] = sum4[3] = 0.f;
             exps(Lo{});
-            const bool grown = mx > m + 8.f;
+            const bool grown = live && mx > m + 8.f;
             if (!__any_sync(0xffffffffu, grown)) break;
             move_max(grown, mx);
           }
