@@ -43,6 +43,7 @@
 // rows zeroed in shared memory before the product: 0 x NaN would be NaN.
 //
 // Every mbarrier wait is bounded, as in the routed attention kernel.
+#include <cfloat>
 #include <cuda_fp16.h>
 
 #include "tc_sm100.cuh"
@@ -246,45 +247,60 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The cap c tanh(x kz), kz = scale / c, of scores x, in units of log 2.  Where
-// |x kz| <= 0.6 in all of a tile's scores it is x times a polynomial in x^2: tanh(z) / z
-// fitted in z^2 for least error (2^-23.6 relative), with kz and the scale in its
-// coefficients; 6 packed operations for two scores, none on the multi-function unit.
+// The cap c tanh(z), z = x kz, kz = scale / c, of scores x, in units of log 2.  Where
+// |z| <= 0.6 it is z times a polynomial in z^2: tanh(z) / z fitted in z^2 for least error
+// (2^-23.4 relative, in exact arithmetic), with c log2 e in its coefficients; 7 packed
+// operations for two scores, none on the multi-function unit.  Beyond, it is
+// c - 2 c / (1 + e^(2 z)), whose error is a few 2^-24 of c: near 0 that would be all of a
+// score, so each score takes the form that is exact relative to itself.
 struct Cap {
-  float c0, c1, c2, c3, c4, most;  // coefficients, and the largest x^2 they hold for
-  __device__ __forceinline__ void init(float kz, float scale_log2) {
-    const float k2 = kz * kz;
-    c0 = scale_log2;
-    c1 = -0.33332622051239014f * k2 * c0;
-    c2 = 0.13313521444797516f * k2 * k2 * c0;
-    c3 = -0.05223110690712929f * k2 * k2 * k2 * c0;
-    c4 = 0.01564048044383526f * k2 * k2 * k2 * k2 * c0;
-    most = 0.36f / k2;
+  float kz, c0, c1, c2, c3, c4;
+  __device__ __forceinline__ void init(float scale, float cap) {
+    kz = fminf(scale / cap, FLT_MAX);  // a score of 0 stays one under the smallest caps
+    c0 = cap * LOG2E;
+    c1 = -0.33332622051239014f * c0;
+    c2 = 0.13313521444797516f * c0;
+    c3 = -0.05223110690712929f * c0;
+    c4 = 0.01564048044383526f * c0;
+  }
+  // z and z^2 of two scores, and the polynomial's value
+  __device__ __forceinline__ void near(const float* x, float* z, float* u, float* y) const {
+    float p0, p1;
+    mul2(z[0], z[1], x[0], x[1], kz, kz);
+    mul2(u[0], u[1], z[0], z[1], z[0], z[1]);
+    fma2(p0, p1, u[0], u[1], c4, c3);
+    fma2e(p0, p1, u[0], u[1], c2);
+    fma2e(p0, p1, u[0], u[1], c1);
+    fma2e(p0, p1, u[0], u[1], c0);
+    mul2(y[0], y[1], z[0], z[1], p0, p1);
   }
 };
-// False, with x spoiled, where a score lies beyond.  Rows that are not `live` have no say:
-// theirs come of whatever the shared memory behind packed rows held.
+constexpr float CAP_NEAR = 0.36f;  // the largest z^2 of the polynomial
+// Caps a tile's scores if all of a warp's are near; else false, with x spoiled.  Rows that
+// are not `live` have no say: theirs come of whatever the shared memory behind packed rows held.
 __device__ __forceinline__ bool cap_near(float* x, const Cap& c, bool live) {
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
-    float u0, u1, p0, p1;
-    mul2(u0, u1, x[k], x[k + 1], x[k], x[k + 1]);
-    far[(k >> 1) & 3] = max3(far[(k >> 1) & 3], u0, u1);
-    fma2(p0, p1, u0, u1, c.c4, c.c3);
-    fma2e(p0, p1, u0, u1, c.c2);
-    fma2e(p0, p1, u0, u1, c.c1);
-    fma2e(p0, p1, u0, u1, c.c0);
-    mul2(x[k], x[k + 1], x[k], x[k + 1], p0, p1);
+    float z[2], u[2];
+    c.near(x + k, z, u, x + k);
+    far[(k >> 1) & 3] = max3(far[(k >> 1) & 3], u[0], u[1]);
   }
-  const bool beyond = live && max3(fmaxf(far[0], far[1]), far[2], far[3]) > c.most;
+  const bool beyond = live && max3(fmaxf(far[0], far[1]), far[2], far[3]) > CAP_NEAR;
   return !__any_sync(0xffffffffu, beyond);
 }
-// The same for any scores: c tanh(z) = c - 2 c / (1 + e^(2 z)), zin = 2 kz log2 e and
-// cl = c log2 e.
-__device__ __forceinline__ void cap_far(float* x, float zin, float cl) {
+// The same for any scores, each by its own form.
+__device__ __forceinline__ void cap_far(float* x, const Cap& c) {
 #pragma unroll
-  for (int k = 0; k < TBN; ++k) x[k] = fmaf(-2.f * cl, rcp(1.f + ex2(x[k] * zin)), cl);
+  for (int k = 0; k < TBN; k += 2) {
+    float z[2], u[2], y[2];
+    c.near(x + k, z, u, y);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float f = fmaf(-2.f * c.c0, rcp(1.f + ex2(z[e] * (2.f * LOG2E))), c.c0);
+      x[k + e] = u[e] <= CAP_NEAR ? y[e] : f;
+    }
+  }
 }
 // Scores times `scale`, less the slope times the distance |at - k| of key k.  The
 // distance of a tile that lies wholly before or behind the row is linear in k.
@@ -616,7 +632,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     const uint32_t scol = tbase + lane_f + s * 128, ocol = tbase + lane_f + O_COL + s * 128;
     const float scale_log2 = a.scale * LOG2E;
     Cap cap;
-    if (MODE == CAP) cap.init(a.scale / a.softcap, scale_log2);
+    if (MODE != PLAIN) cap.init(a.scale, a.softcap);
     int np = 0, no = 0, c = 0;  // tiles and items this stream has had, ring entries so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -667,11 +683,11 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         auto take = [&]() {  // the row's scores, transformed and masked
           load();
           if (MODE != PLAIN && a.softcap > 0.f) {
-            if (MODE == CAP && !far && !cap_near(x, cap, live)) {
+            if (!far && !cap_near(x, cap, live)) {
               far = true;  // for the rest of the item: such scores seldom come alone
               load();
             }
-            if (MODE == BIAS || far) cap_far(x, 2.f * LOG2E * a.scale / a.softcap, a.softcap * LOG2E);
+            if (far) cap_far(x, cap);
           }
           if (MODE == BIAS && a.slopes)  // (always: the branch keeps the loads from spilling)
             bias_scores(x, a.softcap > 0.f ? 1.f : scale_log2, slope,
@@ -1248,7 +1264,8 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   a.causal = p->causal;
   a.q_start = p->q_start;
   a.scale = p->scale > 0.f ? p->scale : 1.f / sqrtf((float)p->d);
-  a.softcap = p->softcap;
+  // A cap 2^60 times past what a score of 1 becomes leaves all scores as they are in fp32.
+  a.softcap = p->softcap > 0x1p60f * a.scale ? 0.f : p->softcap;
   a.pack = q.pack;
   a.ntile_h = q.ntile_h;
   a.nqb = q.nqb;
