@@ -80,7 +80,7 @@ struct AmArgs {
   int o_wide;  // rows of O lie on 32 bytes
   int B, Hq, Hk, Nq, Nk, causal, q_start;
   int qmul_b, qmul_h, kmul_b, kmul_h, vmul_b, vmul_h;  // 0 where a TMA dimension has one entry
-  float scale, softcap;
+  float scale, softcap, kz;  // kz: scale / softcap
   // the plan: tiles of rows (heads packed per tile `pack`, query blocks `nqb`), key splits
   int pack, ntile_h, nqb, nsplit, n_items, by_block;
   int n_tiles, n_whole;  // row tiles; the first n_whole are one item each, the rest nsplit
@@ -248,56 +248,84 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 }
 
 // The cap c tanh(z), z = x kz, kz = scale / c, of scores x, in units of log 2.  Where
-// |z| <= 0.6 it is z times a polynomial in z^2: tanh(z) / z fitted in z^2 for least error
-// (2^-23.4 relative, in exact arithmetic), with c log2 e in its coefficients; 7 packed
-// operations for two scores, none on the multi-function unit.  Beyond, it is
+// |z| <= 0.6 it is x times a polynomial in x^2: tanh(z) / z fitted in z^2 for least error
+// (2^-23.4 relative, in exact arithmetic), with kz and the scale in its coefficients; 6
+// packed operations for two scores, none on the multi-function unit.  (Working in z takes
+// 7: 2 x 16 heads x 4,097 x 4,097, d = 64, with a prefix, 272 us against 265.)  Beyond, it is
 // c - 2 c / (1 + e^(2 z)), whose error is a few 2^-24 of c: near 0 that would be all of a
 // score, so each score takes the form that is exact relative to itself.
+constexpr float T1 = -0.33332622051239014f, T2 = 0.13313521444797516f, T3 = -0.05223110690712929f,
+                T4 = 0.01564048044383526f;
+constexpr float CAP_NEAR = 0.36f;  // the largest z^2 of the polynomial
 struct Cap {
-  float kz, c0, c1, c2, c3, c4;
+  float c0, c1, c2, c3, c4, most;  // coefficients, and the largest x^2 they hold for
   __device__ __forceinline__ void init(float scale, float cap) {
-    kz = fminf(scale / cap, FLT_MAX);  // a score of 0 stays one under the smallest caps
-    c0 = cap * LOG2E;
-    c1 = -0.33332622051239014f * c0;
-    c2 = 0.13313521444797516f * c0;
-    c3 = -0.05223110690712929f * c0;
-    c4 = 0.01564048044383526f * c0;
-  }
-  // z and z^2 of two scores, and the polynomial's value
-  __device__ __forceinline__ void near(const float* x, float* z, float* u, float* y) const {
-    float p0, p1;
-    mul2(z[0], z[1], x[0], x[1], kz, kz);
-    mul2(u[0], u[1], z[0], z[1], z[0], z[1]);
-    fma2(p0, p1, u[0], u[1], c4, c3);
-    fma2e(p0, p1, u[0], u[1], c2);
-    fma2e(p0, p1, u[0], u[1], c1);
-    fma2e(p0, p1, u[0], u[1], c0);
-    mul2(y[0], y[1], z[0], z[1], p0, p1);
+    const float kz = scale / cap, k2 = kz * kz;
+    c0 = scale * LOG2E;
+    c1 = T1 * k2 * c0;
+    c2 = T2 * k2 * k2 * c0;
+    c3 = T3 * k2 * k2 * k2 * c0;
+    c4 = T4 * k2 * k2 * k2 * k2 * c0;
+    most = CAP_NEAR / k2;
   }
 };
-constexpr float CAP_NEAR = 0.36f;  // the largest z^2 of the polynomial
+// Whether a cap's coefficients (kz^9 c in c4) are normal fp32 numbers.
+bool cap_is_usual(float scale, float cap) {
+  const float kz = scale / cap;
+  return kz >= 0x1p-12f && kz <= 0x1p8f && cap >= 0x1p-12f && cap <= 0x1p50f;
+}
+// squares of two scores, and the polynomial's value
+__device__ __forceinline__ void cap_poly(const float* x, float* u, float* y, const Cap& c) {
+  float p0, p1;
+  mul2(u[0], u[1], x[0], x[1], x[0], x[1]);
+  fma2(p0, p1, u[0], u[1], c.c4, c.c3);
+  fma2e(p0, p1, u[0], u[1], c.c2);
+  fma2e(p0, p1, u[0], u[1], c.c1);
+  fma2e(p0, p1, u[0], u[1], c.c0);
+  mul2(y[0], y[1], x[0], x[1], p0, p1);
+}
 // Caps a tile's scores if all of a warp's are near; else false, with x spoiled.  Rows that
 // are not `live` have no say: theirs come of whatever the shared memory behind packed rows held.
 __device__ __forceinline__ bool cap_near(float* x, const Cap& c, bool live) {
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
-    float z[2], u[2];
-    c.near(x + k, z, u, x + k);
+    float u[2];
+    cap_poly(x + k, u, x + k, c);
     far[(k >> 1) & 3] = max3(far[(k >> 1) & 3], u[0], u[1]);
   }
-  const bool beyond = live && max3(fmaxf(far[0], far[1]), far[2], far[3]) > CAP_NEAR;
+  const bool beyond = live && max3(fmaxf(far[0], far[1]), far[2], far[3]) > c.most;
   return !__any_sync(0xffffffffu, beyond);
 }
-// The same for any scores, each by its own form.
-__device__ __forceinline__ void cap_far(float* x, const Cap& c) {
+// The same for any scores, each by its own form (near ones to the same bits: keys that a row
+// does not see may send its warp here).  z2: 2 kz log2 e.
+__device__ __forceinline__ void cap_far(float* x, const Cap& c, float z2, float cl) {
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
-    float z[2], u[2], y[2];
-    c.near(x + k, z, u, y);
+    float u[2], y[2];
+    cap_poly(x + k, u, y, c);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float f = fmaf(-2.f * c.c0, rcp(1.f + ex2(z[e] * (2.f * LOG2E))), c.c0);
+      const float f = fmaf(-2.f * cl, rcp(1.f + ex2(x[k + e] * z2)), cl);
+      x[k + e] = u[e] <= c.most ? y[e] : f;
+    }
+  }
+}
+// Any cap of any scores: in z, whose polynomial has coefficients of usual size.
+__device__ __forceinline__ void cap_any(float* x, float kz, float cl) {
+#pragma unroll
+  for (int k = 0; k < TBN; k += 2) {
+    float z[2], u[2], p[2], y[2];
+    mul2(z[0], z[1], x[k], x[k + 1], kz, kz);
+    mul2(u[0], u[1], z[0], z[1], z[0], z[1]);
+    fma2(p[0], p[1], u[0], u[1], T4 * cl, T3 * cl);
+    fma2e(p[0], p[1], u[0], u[1], T2 * cl);
+    fma2e(p[0], p[1], u[0], u[1], T1 * cl);
+    fma2e(p[0], p[1], u[0], u[1], cl);
+    mul2(y[0], y[1], z[0], z[1], p[0], p[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float f = fmaf(-2.f * cl, rcp(1.f + ex2(z[e] * (2.f * LOG2E))), cl);
       x[k + e] = u[e] <= CAP_NEAR ? y[e] : f;
     }
   }
@@ -367,14 +395,16 @@ __device__ __forceinline__ float max_of(const float* x) {
 template <typename T>
 constexpr float p_shift() { return sizeof(T) == 2 && std::is_same<T, __half>::value ? 7.f : 0.f; }
 
-// MODE: PLAIN scores, CAP tanh cap, BIAS distance penalty (and a cap, where given).
-enum { PLAIN, CAP, BIAS };
+// MODE: PLAIN scores, CAP tanh cap, BIAS distance penalty, BOTH of them (or a cap far from the
+// scores' size without a penalty).
+enum { PLAIN, CAP, BIAS, BOTH };
 template <typename T, int D, bool SOLO, int MODE>
 __global__ void __launch_bounds__(AM_THREADS, 1)
     k_attend_masked(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AmArgs a) {
   constexpr uint32_t TILE = tile_bytes<D>();
   constexpr int NST = ring<D>(), NBOX = D / 64;
+  constexpr bool BIASED = MODE == BIAS || MODE == BOTH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -632,7 +662,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     const uint32_t scol = tbase + lane_f + s * 128, ocol = tbase + lane_f + O_COL + s * 128;
     const float scale_log2 = a.scale * LOG2E;
     Cap cap;
-    if (MODE != PLAIN) cap.init(a.scale, a.softcap);
+    if (MODE == CAP) cap.init(a.scale, a.softcap);
     int np = 0, no = 0, c = 0;  // tiles and items this stream has had, ring entries so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -651,11 +681,12 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       const int whole = it.lim.limit(it.q0 + (SOLO ? 0 : s * TBM));  // keys every row of the tile sees
       const int lim = live ? it.lim.limit(qi) : 0;
       const int docq = a.doc_q && live ? a.doc_q[(int64_t)it.b * a.Nq + qi] : 0;
-      const float slope = MODE == BIAS ? a.slopes[h] * LOG2E : 0.f;
+      const float slope = BIASED && a.slopes ? a.slopes[h] * LOG2E : 0.f;
       const int32_t* dk = a.doc_k ? a.doc_k + (int64_t)it.b * a.Nk : nullptr;
       const bool work = __any_sync(0xffffffffu, live);  // a warp without rows only keeps step
       float m = -INFINITY, l = 0.f;
-      bool first = true, far = false;
+      bool first = true;
+      int far = 0;
       for (int i = 0; i < it.n; ++i) {
         int bits;
         const int t = it.entry(i, bits);
@@ -680,23 +711,31 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           for (int k = 0; k < 4; ++k) tc::tmem_ld32(scol + 32 * k, sr + 32 * k);
           tc::tmem_wait_ld();
         };
+        auto hide = [&](float value) {  // the scores of the keys that the row does not see
+#pragma unroll
+          for (int k = 0; k < TBN; ++k)
+            if (!(seen[k / 32] & (1u << (k % 32)))) x[k] = value;
+        };
         auto take = [&]() {  // the row's scores, transformed and masked
           load();
-          if (MODE != PLAIN && a.softcap > 0.f) {
-            if (!far && !cap_near(x, cap, live)) {
-              far = true;  // for the rest of the item: such scores seldom come alone
-              load();
-            }
-            if (far) cap_far(x, cap);
+          if (MODE == CAP && !far && !cap_near(x, cap, live)) {
+            far = 1;  // for the rest of the item: such scores seldom come alone
+            load();
           }
-          if (MODE == BIAS && a.slopes)  // (always: the branch keeps the loads from spilling)
-            bias_scores(x, a.softcap > 0.f ? 1.f : scale_log2, slope,
-                        (float)(it.lim.pos0 + qi - t0));
-          if (part) {
-#pragma unroll
-            for (int k = 0; k < TBN; ++k)
-              if (!(seen[k / 32] & (1u << (k % 32)))) x[k] = -INFINITY;
+          // in a block of its own, and its numbers made there: in one with the loads, or kept
+          // through all tiles, it spills 250 bytes of the near form's registers
+          if (MODE == CAP) asm volatile("" : "+r"(far));
+          if ((MODE == BOTH && a.softcap > 0.f) || (MODE == CAP && far)) {
+            float kz = a.kz, cl = a.softcap * LOG2E;
+            asm volatile("" : "+f"(kz), "+f"(cl));
+            if (MODE == CAP)
+              cap_far(x, cap, 2.f * LOG2E * kz, cl);
+            else
+              cap_any(x, kz, cl);
           }
+          if (BIASED && a.slopes)  // (BIAS always: the branch keeps the loads from spilling)
+            bias_scores(x, MODE == BIAS ? scale_log2 : 1.f, slope, (float)(it.lim.pos0 + qi - t0));
+          if (part) hide(-INFINITY);
         };
         const float sl2 = MODE == PLAIN ? scale_log2 : 1.f;
         uint32_t pr[32];
@@ -738,10 +777,10 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           }
           m = top;
         };
-        // BIAS: where every probability of the warp's rows would be flushed to 0 (a
+        // BIAS, BOTH: where every probability of the warp's rows would be flushed to 0 (a
         // distance penalty far from the rows), there is no exponential to take.
         bool nothing = false;
-        if (MODE == BIAS) {
+        if (BIASED) {
           if (work) {
             take();
             const float mx = max_of(x);
@@ -1177,6 +1216,9 @@ cudaError_t launch(const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
 template <typename T, int D>
 cudaError_t launch_for(bool solo, const AmArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                        const CUtensorMap& v, int sms, cudaStream_t st) {
+  if (a.softcap > 0.f && (a.slopes || !cap_is_usual(a.scale, a.softcap)))
+    return solo ? launch<T, D, true, BOTH>(a, q, k, v, sms, st)
+                : launch<T, D, false, BOTH>(a, q, k, v, sms, st);
   if (a.slopes)
     return solo ? launch<T, D, true, BIAS>(a, q, k, v, sms, st)
                 : launch<T, D, false, BIAS>(a, q, k, v, sms, st);
@@ -1266,6 +1308,7 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   a.scale = p->scale > 0.f ? p->scale : 1.f / sqrtf((float)p->d);
   // A cap 2^60 times past what a score of 1 becomes leaves all scores as they are in fp32.
   a.softcap = p->softcap > 0x1p60f * a.scale ? 0.f : p->softcap;
+  a.kz = fminf(a.scale / a.softcap, FLT_MAX);  // a score of 0 stays one under the smallest caps
   a.pack = q.pack;
   a.ntile_h = q.ntile_h;
   a.nqb = q.nqb;

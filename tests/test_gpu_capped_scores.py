@@ -117,3 +117,27 @@ def test_bits_do_not_depend_on_left_over_shared_memory(Nq, Hq, Hk, Nk, d, slopes
         got.append(run(Q, K, V, **kw))
     for O, L in got[1:]:
         assert torch.equal(O, got[0][0]) and torch.equal(L, got[0][1])
+
+
+@pytest.mark.parametrize("Nq", [1, 5, 200])
+def test_bits_do_not_depend_on_keys_that_do_not_count(Nq):
+    """Lengths, negative documents and keys behind a causal query, in tiles that hold others too."""
+    Q, K, V = tensors(2, 4, 2, Nq, 500, 64, BF, seed=54)
+    lens = torch.tensor([430, 300], dtype=torch.int32, device="cuda")
+    doc = torch.zeros(2, 500, dtype=torch.int32, device="cuda")
+    doc[:, 100:140] = -1
+    kinds = [dict(k_len=lens), dict(k_len=lens, causal=True),
+             dict(doc_q=doc[:, :Nq].clamp(min=0).contiguous(), doc_k=doc)]
+    for kw in kinds:
+        got = []
+        for value in (0.0, 1e4, -1e30, float("nan")):
+            for b, n in enumerate((430, 300)):
+                if "k_len" in kw:
+                    K[b, :, n:], V[b, :, n:] = value, value
+                else:
+                    K[b, :, 100:140], V[b, :, 100:140] = value, value
+            got.append(run(Q, K, V, softcap=30.0, **kw))
+        for O, L in got[1:]:
+            assert torch.equal(O, got[0][0]) and torch.equal(L, got[0][1])
+        K[:, :, 100:140], V[:, :, 100:140] = 0.5, 0.5
+        K[:, :, 300:], V[:, :, 300:] = 0.5, 0.5
