@@ -39,8 +39,8 @@
 // which grows with the row, so a tile is skipped, partly masked or whole by
 // comparing two limits.  Documents are classified per (256 rows, 128 keys) by
 // their id ranges in k_am_documents, which lists the tiles to visit.
-// Keys that count for nobody (past the length, negative document) have their V
-// rows zeroed in shared memory before the product: 0 x NaN would be NaN.
+// Keys that count for nobody (past the length or the last row's limit, negative
+// document) have their V rows zeroed in shared memory before the product: 0 x NaN would be NaN.
 //
 // Every mbarrier wait is bounded, as in the routed attention kernel.
 #include <cfloat>
@@ -97,11 +97,13 @@ struct AmArgs {
 // the keys below limit(row), which does not decrease with the row.
 struct Limits {
   int len, pre, pos0, causal;
+  int end;  // keys from here on are seen by no row of the batch
   __device__ __forceinline__ void init(const AmArgs& a, int b) {
     len = a.k_len ? min(max(a.k_len[b], 0), a.Nk) : a.Nk;
     pre = a.prefix ? min(max(a.prefix[b], 0), len) : 0;
     pos0 = a.q_start == SPR_ALIGN_END ? len - a.Nq : a.q_start;
     causal = a.causal;
+    end = limit(a.Nq - 1);
   }
   __device__ __forceinline__ int limit(int row) const {
     return causal ? max(min(pos0 + row + 1, len), pre) : len;
@@ -172,7 +174,7 @@ struct Item {
     }
     int t = i0 + i;
     if (t <= near) t = near - t;  // the rows' own tile first, then back, then on
-    bits = 12 | (t < nt[0] ? 1 : 0) | (t < nt[1] ? 2 : 0) | ((t + 1) * TBN > lim.len ? 16 : 0);
+    bits = 12 | (t < nt[0] ? 1 : 0) | (t < nt[1] ? 2 : 0) | ((t + 1) * TBN > lim.end ? 16 : 0);
     return t;
   }
   __device__ __forceinline__ uint32_t streams(int i) const {
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           const int kv = c + 2 * i + 1;
           got_v = tc::mbar_wait(full + kv % NST, (kv / NST) & 1, abort_s, WAIT_NS);
           const int j = t0 + row;
-          if (got_v && (j >= it.lim.len || (dk && dk[j] < 0))) {
+          if (got_v && (j >= it.lim.end || (dk && dk[j] < 0))) {
             uint8_t* v = sKV + (size_t)(kv % NST) * TILE + row * 128;
 #pragma unroll
             for (int k = 0; k < NBOX; ++k)
@@ -1056,10 +1058,10 @@ __global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ A
     int bits = 0;
     if (t < most) {
       int kl = INT32_MAX, kh = -1;
-      bool dead = (t + 1) * TBN > lim.len;
+      bool dead = (t + 1) * TBN > lim.end;
       for (int k = 0; k < 4; ++k) {
         const int j = t * TBN + 32 * k + lane;
-        const int id = j < lim.len ? a.doc_k[(int64_t)b * a.Nk + j] : -1;
+        const int id = j < lim.end ? a.doc_k[(int64_t)b * a.Nk + j] : -1;
         if (id >= 0) {
           kl = min(kl, id);
           kh = max(kh, id);

@@ -422,10 +422,11 @@ size_t sparsepr_attend_masked_workspace(const spr_masked_params* prm);
  *   prefix  [B] int32, with causal only, or NULL
  *   slopes  [Hq] fp32, or NULL (no bias)
  *   lse     [B, Hq, Nq] fp32, or NULL: natural log of the sum of exp(x_ij)
- * Keys at or past len_b and keys of a negative document do not count whatever
- * K and V hold there.  A key that some query sees is multiplied by 0 for the
- * others, so an infinite or NaN row of V may reach O rows that do not see it
- * (K may hold anything there).  fp32 accumulation and statistics; the probabilities are
+ * Keys at or past len_b, keys behind the position of the batch's last query
+ * (with causal, outside the prefix) and keys of a negative document do not count
+ * whatever K and V hold there, so the unfilled part of a cache may hold anything.
+ * Any other key is multiplied by 0 for the queries that do not see it, so an
+ * infinite or NaN row of V there may reach their O (K may hold anything).  fp32 accumulation and statistics; the probabilities are
  * rounded to the input type for their product with V.
  */
 spr_status sparsepr_attend_masked(const spr_masked_params* prm, const void* Q, const void* K,
