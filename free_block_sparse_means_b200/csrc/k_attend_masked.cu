@@ -108,6 +108,15 @@ struct Limits {
   __device__ __forceinline__ int limit(int row) const {
     return causal ? max(min(pos0 + row + 1, len), pre) : len;
   }
+  // The place of row's position among the keys 0 .. len - 1 or next to them.  For all of these keys
+  // |p - j| = |p - near| + |near - j|: the first part, the same for all of a row's scores, is
+  // left to its lse (beyond()), so that far positions cost the scores no bits.
+  __device__ __forceinline__ int nearest(int row) const {
+    return max(min(pos0 + row, len - 1), 0);
+  }
+  __device__ __forceinline__ float beyond(int row) const {
+    return (float)abs(pos0 + row - nearest(row));
+  }
 };
 
 // One work item: a row tile (or pair of them) and its share of the key tiles.  The
@@ -686,6 +695,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       const float slope = BIASED && a.slopes ? a.slopes[h] * LOG2E : 0.f;
       const int32_t* dk = a.doc_k ? a.doc_k + (int64_t)it.b * a.Nk : nullptr;
       const bool work = __any_sync(0xffffffffu, live);  // a warp without rows only keeps step
+      const int place = BIASED ? it.lim.nearest(qi) : 0;
       float m = -INFINITY, l = 0.f;
       bool first = true;
       int far = 0;
@@ -736,7 +746,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
               cap_any(x, kz, cl);
           }
           if (BIASED && a.slopes)  // (BIAS always: the branch keeps the loads from spilling)
-            bias_scores(x, MODE == BIAS ? scale_log2 : 1.f, slope, (float)(it.lim.pos0 + qi - t0));
+            bias_scores(x, MODE == BIAS ? scale_log2 : 1.f, slope, (float)(place - t0));
           if (part) hide(-INFINITY);
         };
         const float sl2 = MODE == PLAIN ? scale_log2 : 1.f;
@@ -919,7 +929,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         }
         if (live && a.lse)
           a.lse[((int64_t)it.b * a.Hq + h) * a.Nq + qi] =
-              l == 0.f ? -INFINITY : (m - p_shift<T>()) * LN2 + logf(l);
+              l == 0.f ? -INFINITY
+                       : fmaf(BIASED && a.slopes ? -a.slopes[h] : 0.f, it.lim.beyond(qi),
+                              (m - p_shift<T>()) * LN2 + logf(l));
       }
       if (any) {
         tc::tc_fence_before();
@@ -1010,8 +1022,14 @@ __global__ void __launch_bounds__(128) k_am_join(const __grid_constant__ AmArgs 
   } else {
     *reinterpret_cast<uint32_t*>(O) = u0;
   }
-  if (a.lse && lane == 0)
-    a.lse[((int64_t)b * a.Hq + h) * a.Nq + qi] = l == 0.f ? -INFINITY : (M - p_shift<T>()) * LN2 + logf(l);
+  if (a.lse && lane == 0) {
+    float lse = l == 0.f ? -INFINITY : (M - p_shift<T>()) * LN2 + logf(l);
+    if (a.slopes && l != 0.f) {
+      it.lim.init(a, b);
+      lse = fmaf(-a.slopes[h], it.lim.beyond(qi), lse);
+    }
+    a.lse[((int64_t)b * a.Hq + h) * a.Nq + qi] = lse;
+  }
 }
 
 // The key tiles that a row tile has to visit under documents: a block per (row
