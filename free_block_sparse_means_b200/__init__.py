@@ -10,8 +10,8 @@ from ._binding import (EXPORTS, LIB_PATH, PARTITION_RESPONSE, PARTITION_SEMANTIC
                        load_library, make_params, sparsepr_attend, sparsepr_attend_routed_noalloc,
                        sparsepr_call, sparsepr_check_params, sparsepr_get_stats,
                        sparsepr_launch_count, sparsepr_partition, sparsepr_reconstruct,
-                       sparsepr_route, sparsepr_version, sparsepr_workspace_size,
-                       sparsepr_workspace_view, workspace_tensor)
+                       sparsepr_route, sparsepr_version, sparsepr_workspace_error,
+                       sparsepr_workspace_size, sparsepr_workspace_view, workspace_tensor)
 from .attention_block import AttentionBlock
 from .host_call import HostPipeline
 from .operators import (make_masked, make_norm_rotate, make_project, sparsepr_attend_masked,
@@ -26,5 +26,5 @@ __all__ = [
     "sparsepr_attend_masked", "sparsepr_attend_routed_noalloc", "sparsepr_call",
     "sparsepr_check_params", "sparsepr_get_stats", "sparsepr_launch_count", "sparsepr_partition",
     "sparsepr_reconstruct", "sparsepr_route", "sparsepr_version", "sparsepr_workspace_size",
-    "sparsepr_workspace_view", "workspace_tensor",
+    "sparsepr_workspace_error", "sparsepr_workspace_view", "workspace_tensor",
 ]

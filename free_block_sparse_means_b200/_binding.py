@@ -245,7 +245,8 @@ def sparsepr_check_params(prm: SprParams) -> int:
 
 
 def alloc_workspace(prm, device=None) -> torch.Tensor:
-    """Workspace for a call, a masked attention or a projection with these parameters."""
+    """Workspace for a call, a masked attention or a projection with these parameters; the error
+    words of the latter two are cleared on the current stream."""
     if isinstance(prm, SprMaskedParams):
         n = load_library().sparsepr_attend_masked_workspace(ctypes.byref(prm))
         if n == 0:
@@ -260,7 +261,19 @@ def alloc_workspace(prm, device=None) -> torch.Tensor:
             raise SparsePRError("sparsepr_workspace_size", sparsepr_check_params(prm))
     ws = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
     off = (-ws.data_ptr()) % 256
-    return ws[off:off + n]
+    ws = ws[off:off + n]
+    if isinstance(prm, (SprMaskedParams, SprProjectParams)):
+        ws[:16].zero_()  # the error words
+    return ws
+
+
+def sparsepr_workspace_error(ws) -> int:
+    """The error that calls of masked attention or a projection left in their workspace, 0 if none.
+
+    4: a bounded wait gave up and the output of that call is not whole.  Waits for the current
+    stream of the workspace's device.  The word stays until it is cleared (`ws[:16].zero_()`).
+    """
+    return int(ws.reshape(-1).view(torch.uint8)[:4].view(torch.int32).item())
 
 
 def sparsepr_partition(prm, Q, K, V, ws, stream=None):

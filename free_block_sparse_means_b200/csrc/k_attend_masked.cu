@@ -90,7 +90,7 @@ struct AmArgs {
   int ktiles;
   float *part_o, *part_ml;
   int part_rows;  // rows of a row tile that partial results hold
-  int32_t* status;
+  int32_t *status, *words;  // the call's, and the error words of its workspace
 };
 
 // What the mask leaves of one batch's keys for query rows first .. last: rows see
@@ -942,8 +942,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (threadIdx.x == 0 && *abort_s && a.status && atomicCAS(a.status, 0, (int)ERR_TIMEOUT) == 0)
-    a.status[1] = blockIdx.x;
+  if (threadIdx.x == 0 && *abort_s) report_timeout(a.status, a.words);
   if (warp == 9) {
     __syncwarp();
     tc::tmem_dealloc(tbase, TMEM_COLS);
@@ -1126,7 +1125,7 @@ __global__ void __launch_bounds__(1024) k_am_documents(const __grid_constant__ A
 struct Plan {
   bool solo;
   int pack, ntile_h, nqb, nsplit, n_items, ktiles, part_rows, by_block, n_tiles, n_whole;
-  size_t next_off, count_off, list_off, o_off, ml_off, total;
+  size_t words_off, next_off, count_off, list_off, o_off, ml_off, total;
 };
 
 Plan make_plan(const spr_masked_params& p, int sms) {
@@ -1187,6 +1186,7 @@ Plan make_plan(const spr_masked_params& p, int sms) {
     at += (bytes + 255) / 256 * 256;
     return off;
   };
+  q.words_off = take(16);
   q.next_off = take(4);
   q.count_off = take((size_t)p.B * q.nqb * 16);
   q.list_off = take((size_t)p.B * q.nqb * q.ktiles * 4);
@@ -1355,6 +1355,7 @@ extern "C" spr_status sparsepr_attend_masked(const spr_masked_params* p, const v
   a.part_ml = reinterpret_cast<float*>(base + q.ml_off);
   a.part_rows = q.part_rows;
   a.status = status;
+  a.words = reinterpret_cast<int32_t*>(base + q.words_off);
   const CUtensorMapDataType dt = p->dtype == SPR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mq, mk, mv;

@@ -50,6 +50,7 @@ constexpr uint32_t PJ_TMEM = 512;              // two accumulators of 256 column
 constexpr uint64_t PJ_WAIT_NS = 2000000000ull;  // 2 s
 constexpr size_t PJ_SMEM = 1024 + (size_t)(2 * NST + 4) * PBOX + 256;
 constexpr int MAX_SPLIT = 8;
+constexpr size_t WORDS_BYTES = 256;  // of the workspace, before the splits' sums
 
 // Division of 0 <= n < 2^31 by a fixed 1 <= d <= 2^31: with 2^s >= d and m = floor(2^(31 + s) / d) + 1,
 // n m >> (31 + s) is exact, as m d - 2^(31 + s) <= d <= 2^s (Granlund and Montgomery).  A tile's
@@ -82,7 +83,7 @@ struct PjArgs {
   uint32_t x_bytes, r_bytes;  // of one box
   int xmul_b, xmul_h, ymul_b, ymul_h, rmul_b, rmul_h;  // 0 where a TMA dimension has one entry
   float* part;
-  int32_t* status;
+  int32_t *status, *words;  // the call's, and the error words of its workspace
 };
 
 __device__ __forceinline__ float tof(bf16 v) { return __bfloat162float(v); }
@@ -575,8 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
   __syncthreads();
   tc::cluster_sync();
   tc::tc_fence_after();
-  if (threadIdx.x == 0 && *abort_s && a.status && atomicCAS(a.status, 0, (int)ERR_TIMEOUT) == 0)
-    a.status[1] = blockIdx.x;
+  if (threadIdx.x == 0 && *abort_s) report_timeout(a.status, a.words);
   if (warp == 2) tc::tmem_dealloc_pair(tbase, PJ_TMEM);
 }
 
@@ -663,7 +663,7 @@ size_t make_plan(const spr_project_params& p, int sms, PjArgs* a) {
     a->ys[i] = p.y_strides[i];
     a->rs[i] = p.r_strides[i];
   }
-  if ((int64_t)p.B * p.N <= FEW_ROWS) return 256;
+  if ((int64_t)p.B * p.N <= FEW_ROWS) return WORDS_BYTES;
   // Batches that follow one another row by row are one batch.
   auto in_a_row = [&](const int64_t* s) { return s[0] == (int64_t)p.N * s[2]; };
   // (the residual's strides are the caller's or Y's: the plan and so the
@@ -716,7 +716,7 @@ size_t make_plan(const spr_project_params& p, int sms, PjArgs* a) {
   a->by_batch.set(a->tiles_per_batch);
   a->by_dx.set(a->dx);
   a->by_dy.set(a->dy);
-  return a->nsplit > 1 ? (size_t)a->nsplit * a->row_tiles * PBM * a->M * 4 : 256;
+  return WORDS_BYTES + (a->nsplit > 1 ? (size_t)a->nsplit * a->row_tiles * PBM * a->M * 4 : 0);
 }
 
 // [B, H, N, d] as a TMA map of boxes of `rows` rows (of `batches` batches) of 64
@@ -799,7 +799,8 @@ extern "C" spr_status sparsepr_project(const spr_project_params* p, const void* 
   a.gate = gate;
   a.R = R;
   a.Y = Y;
-  a.part = static_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + WORDS_BYTES);
+  a.words = static_cast<int32_t*>(ws);
   a.status = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool few = a.n_items == 0;

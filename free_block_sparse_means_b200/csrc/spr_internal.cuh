@@ -268,6 +268,13 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;\ngriddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
+// A wait of this block gave up: to the call's status, if it has one, and to the error words
+// at the start of its workspace, unless an earlier error is there.
+__device__ __forceinline__ void report_timeout(int32_t* status, int32_t* words) {
+  if (status && atomicCAS(status, 0, (int)spr::ERR_TIMEOUT) == 0) status[1] = blockIdx.x;
+  if (atomicCAS(words, 0, (int)spr::ERR_TIMEOUT) == 0) words[1] = blockIdx.x;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

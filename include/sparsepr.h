@@ -346,9 +346,13 @@ spr_status sparsepr_attend_routed_noalloc(const void* Qp, const void* Kp, const 
  * take two 16-bit types (and, where stated, fp32).  `status` is int32[4] on the
  * device, or NULL: after the call's kernels, an error code and three info
  * words (0 = no error; 1 = an index out of range; 4 = a bounded wait gave up).
- * All are forward only.  Workspaces are scratch: nothing is kept in them from
- * one call to the next, so calls (and captured graphs) that follow one another
- * may share one, and calls that may overlap need one each.
+ * All are forward only.  Workspaces are scratch: but for the error words, nothing
+ * is kept in them from one call to the next, so calls (and captured graphs) that
+ * follow one another may share one, and calls that may overlap need one each.
+ * The error words are a workspace's first 16 bytes, int32[4]: a call whose bounded
+ * wait gives up, so that its output is not whole, writes {4, block} there if the
+ * first word is 0, with or without a status.  The library never clears them: set
+ * them to 0 when the workspace is made, read them when the results are used.
  * ------------------------------------------------------------------------ */
 enum { SPR_BF16 = 0, SPR_FP16 = 1, SPR_FP32 = 2 };
 enum { SPR_PAIR_INTERLEAVED = 0, SPR_PAIR_HALVES = 1 };
