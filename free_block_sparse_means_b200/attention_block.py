@@ -5,6 +5,9 @@ keeps: one product makes queries, keys and values head by head, one pass norms a
 and keys, the sparse call or masked attention follows, and the output projection adds its gated
 result to the residual.  Nothing is transposed or copied in between.
 
+Errors that a call meets on the device (a position outside the tables, a wait that gave up) are
+kept until check() is asked.
+
 With a cache, keys and values go to their places behind those of earlier calls and every call
 attends to all of them, so that a prompt and the frames or tokens after it take the same path.
 """
@@ -96,13 +99,17 @@ class AttentionBlock:
             made.append(self._attend)
         self.ws = max((spr.alloc_workspace(p, device=dev) for p in made), key=lambda t: t.numel())
         self.ws_sparse = None if sparse is None else spr.alloc_workspace(self._attend, device=dev)
+        # the status of norm + rotation's last call with positions, and the first error of all of them
+        self._rotated = torch.zeros(4, device=dev, dtype=torch.int32)
+        self.status = torch.zeros(4, device=dev, dtype=torch.int32)
+        self._called = False
 
     def __call__(self, x, cos=None, sin=None, *, at=0, positions=None, gate=None, residual=None,
                  k_len=None, doc=None, prefix=None, out=None):
         """out = residual + gate * (attention(x) w_out^T + b_out); [B, N, C].
 
         cos, sin: tables of the rotation; positions: [B, N] table rows (default: token n takes row
-        n, with a cache row at + n); at: number of tokens already in the cache; gate: [B, C];
+        n, with a cache row at + n; a row outside the tables is an error that check() raises); at: number of tokens already in the cache; gate: [B, C];
         k_len, prefix: [B] and doc: [B, N], the masks of sparsepr_attend_masked (k_len and doc not
         with a cache).  Token n is at position n, with a cache at + n, for the causal mask and the
         slopes.  The tokens of a frame see one another and all before them with prefix = at + N.
@@ -141,8 +148,14 @@ class AttentionBlock:
             k_len = self.k_len.fill_(at + N)
             if positions is None and self._rotate.rot and at:
                 cos, sin = cos[at:], sin[at:]
+        # (rows that are not given are inside the tables, as checked above)
+        given = positions is not None and bool(self._rotate.rot)
         sparsepr_norm_rotate(self._rotate, self.q, self.k, self.q, k_to, wq=self.wq, wk=self.wk,
-                             cos=cos, sin=sin, pos_q=positions, pos_k=positions)
+                             cos=cos, sin=sin, pos_q=positions, pos_k=positions,
+                             status=self._rotated if given else None)
+        if given:
+            torch.where(self.status[:1] != 0, self.status, self._rotated, out=self.status)
+        self._called = True
         if self.sparse is not None:
             spr.sparsepr_call(self._attend, self.q, self.keys, self.values, self.o,
                               self.ws_sparse)
@@ -153,3 +166,22 @@ class AttentionBlock:
         sparsepr_project(self._p_out, self.o, self.w_out, y4, self.ws, bias=self.b_out, gate=gate,
                          residual=None if residual is None else residual.view(B, 1, N, C))
         return out
+
+    def check(self):
+        """Wait for the block's calls so far and raise SparsePRError if one of them met an error on the
+        device; the error is then forgotten.
+
+        A token whose position is outside the tables has a query without norm and rotation and, in
+        the cache, whatever key was there: results that see it are not valid, nor are those of other
+        blocks on the same cache.  After a wait that gave up the output of that call is not whole.
+        """
+        code, b, n, row = self.status.tolist()
+        waited = spr.sparsepr_workspace_error(self.ws)
+        self.status.zero_()
+        self.ws[:16].zero_()
+        met = [f"position {row} of token {n}, batch {b}, is not a row of the tables"] * bool(code) \
+            + ["a wait gave up"] * bool(waited)
+        if met:
+            raise spr.SparsePRError("AttentionBlock: " + "; ".join(met), spr.SPR_EDEVICE)
+        if self.sparse is not None and self._called:
+            spr.sparsepr_get_stats(self._attend, self.ws_sparse)
