@@ -9,12 +9,17 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import re
+import sys
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libsparsepr.so")
-MARSHAL_PATH = os.path.join(_PKG, "lib", "_marshal.so")
+# bound to the C++ interfaces of one torch and one Python: named after them, so that others do not
+# load it and build their own
+MARSHAL_PATH = os.path.join(_PKG, "lib", f"_marshal.{sys.implementation.cache_tag}-torch-"
+                            f"{re.sub(r'[^0-9A-Za-z.]', '_', torch.__version__)}.so")
 
 (SPR_OK, SPR_EINVAL, SPR_EUNSUPPORTED, SPR_EWORKSPACE, SPR_ECUDA, SPR_EDEVICE,
  SPR_ESCRATCH) = range(7)
@@ -118,7 +123,7 @@ def load_marshal():
     global _marshal
     if _marshal is None:
         if not os.path.exists(MARSHAL_PATH):
-            raise RuntimeError(f"_marshal.so not built ({MARSHAL_PATH}); run "
+            raise RuntimeError(f"_marshal not built for this Python and torch ({MARSHAL_PATH}); run "
                                "`python -m free_block_sparse_means_b200.build`")
         spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
         _marshal = importlib.util.module_from_spec(spec)

@@ -5,7 +5,7 @@
 Objects go to _build/ at the repository root; the shared library goes to
 free_block_sparse_means_b200/lib/.  Rebuilds only when a source is newer than
 the library.  _marshal (the operators' calls from Python, against the installed
-torch's headers) goes beside it.
+torch's headers, under a name that tells both) goes beside it.
 """
 from __future__ import annotations
 
@@ -16,6 +16,8 @@ import shutil
 import subprocess
 import sys
 
+from ._binding import MARSHAL_PATH
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -23,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsparsepr.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
-MARSHAL = os.path.join(LIBDIR, "_marshal.so")
+MARSHAL = MARSHAL_PATH
 BUILD = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
