@@ -157,8 +157,9 @@ class AttentionBlock:
             torch.where(self.status[:1] != 0, self.status, self._rotated, out=self.status)
         self._called = True
         if self.sparse is not None:
-            spr.sparsepr_call(self._attend, self.q, self.keys, self.values, self.o,
-                              self.ws_sparse)
+            with torch.cuda.device(x.device):  # the call itself takes the current one
+                spr.sparsepr_call(self._attend, self.q, self.keys, self.values, self.o,
+                                  self.ws_sparse)
         else:
             sparsepr_attend_masked(self._attend, self.q, self.keys, self.values, self.o, self.ws,
                                    k_len=k_len, doc_q=doc, doc_k=doc, prefix=prefix,
@@ -184,4 +185,5 @@ class AttentionBlock:
         if met:
             raise spr.SparsePRError("AttentionBlock: " + "; ".join(met), spr.SPR_EDEVICE)
         if self.sparse is not None and self._called:
-            spr.sparsepr_get_stats(self._attend, self.ws_sparse)
+            with torch.cuda.device(self.ws_sparse.device):
+                spr.sparsepr_get_stats(self._attend, self.ws_sparse)
