@@ -262,22 +262,23 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // |z| <= 0.6 it is x times a polynomial in x^2: tanh(z) / z fitted in z^2 for least error
 // (2^-23.4 relative, in exact arithmetic), with kz and the scale in its coefficients; 6
 // packed operations for two scores, none on the multi-function unit.  (Working in z takes
-// 7: 2 x 16 heads x 4,097 x 4,097, d = 64, with a prefix, 272 us against 265.)  Beyond, it is
+// 7, as does a cap with a penalty: 2 x 16 heads x 4,097 x 4,097, d = 64, with a prefix, 272 us
+// against 265.)  Beyond, it is
 // c - 2 c / (1 + e^(2 z)), whose error is a few 2^-24 of c: near 0 that would be all of a
 // score, so each score takes the form that is exact relative to itself.
-constexpr float T1 = -0.33332622051239014f, T2 = 0.13313521444797516f, T3 = -0.05223110690712929f,
-                T4 = 0.01564048044383526f;
-constexpr float CAP_NEAR = 0.36f;  // the largest z^2 of the polynomial
+// Z: in z, with coefficients of usual size under any cap.
+template <bool Z>
 struct Cap {
-  float c0, c1, c2, c3, c4, most;  // coefficients, and the largest x^2 they hold for
-  __device__ __forceinline__ void init(float scale, float cap) {
-    const float kz = scale / cap, k2 = kz * kz;
-    c0 = scale * LOG2E;
-    c1 = T1 * k2 * c0;
-    c2 = T2 * k2 * k2 * c0;
-    c3 = T3 * k2 * k2 * k2 * c0;
-    c4 = T4 * k2 * k2 * k2 * k2 * c0;
-    most = CAP_NEAR / k2;
+  float kz, c0, c1, c2, c3, c4, most;  // coefficients, and the largest x^2 (z^2) they hold for
+  __device__ __forceinline__ void init(float scale, float cap, float ratio) {
+    kz = ratio;
+    const float k2 = Z ? 1.f : kz * kz;
+    c0 = (Z ? cap : scale) * LOG2E;
+    c1 = -0.33332622051239014f * k2 * c0;
+    c2 = 0.13313521444797516f * k2 * k2 * c0;
+    c3 = -0.05223110690712929f * k2 * k2 * k2 * c0;
+    c4 = 0.01564048044383526f * k2 * k2 * k2 * k2 * c0;
+    most = 0.36f / k2;
   }
 };
 // Whether a cap's coefficients (kz^9 c in c4) are normal fp32 numbers.
@@ -285,19 +286,22 @@ bool cap_is_usual(float scale, float cap) {
   const float kz = scale / cap;
   return kz >= 0x1p-12f && kz <= 0x1p8f && cap >= 0x1p-12f && cap <= 0x1p50f;
 }
-// squares of two scores, and the polynomial's value
-__device__ __forceinline__ void cap_poly(const float* x, float* u, float* y, const Cap& c) {
-  float p0, p1;
-  mul2(u[0], u[1], x[0], x[1], x[0], x[1]);
+// x^2 (z^2) of two scores, and the polynomial's value
+template <bool Z>
+__device__ __forceinline__ void cap_poly(const float* x, float* u, float* y, const Cap<Z>& c) {
+  float z0 = x[0], z1 = x[1], p0, p1;
+  if (Z) mul2(z0, z1, x[0], x[1], c.kz, c.kz);
+  mul2(u[0], u[1], z0, z1, z0, z1);
   fma2(p0, p1, u[0], u[1], c.c4, c.c3);
   fma2e(p0, p1, u[0], u[1], c.c2);
   fma2e(p0, p1, u[0], u[1], c.c1);
   fma2e(p0, p1, u[0], u[1], c.c0);
-  mul2(y[0], y[1], x[0], x[1], p0, p1);
+  mul2(y[0], y[1], z0, z1, p0, p1);
 }
 // Caps a tile's scores if all of a warp's are near; else false, with x spoiled.  Rows that
 // are not `live` have no say: theirs come of whatever the shared memory behind packed rows held.
-__device__ __forceinline__ bool cap_near(float* x, const Cap& c, bool live) {
+template <bool Z>
+__device__ __forceinline__ bool cap_near(float* x, const Cap<Z>& c, bool live) {
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
@@ -309,8 +313,9 @@ __device__ __forceinline__ bool cap_near(float* x, const Cap& c, bool live) {
   return !__any_sync(0xffffffffu, beyond);
 }
 // The same for any scores, each by its own form (near ones to the same bits: keys that a row
-// does not see may send its warp here).  z2: 2 kz log2 e.
-__device__ __forceinline__ void cap_far(float* x, const Cap& c, float z2, float cl) {
+// does not see may send its warp here).  z2: 2 kz log2 e; cl: c log2 e.
+template <bool Z>
+__device__ __forceinline__ void cap_far(float* x, const Cap<Z>& c, float z2, float cl) {
 #pragma unroll
   for (int k = 0; k < TBN; k += 2) {
     float u[2], y[2];
@@ -319,25 +324,6 @@ __device__ __forceinline__ void cap_far(float* x, const Cap& c, float z2, float 
     for (int e = 0; e < 2; ++e) {
       const float f = fmaf(-2.f * cl, rcp(1.f + ex2(x[k + e] * z2)), cl);
       x[k + e] = u[e] <= c.most ? y[e] : f;
-    }
-  }
-}
-// Any cap of any scores: in z, whose polynomial has coefficients of usual size.
-__device__ __forceinline__ void cap_any(float* x, float kz, float cl) {
-#pragma unroll
-  for (int k = 0; k < TBN; k += 2) {
-    float z[2], u[2], p[2], y[2];
-    mul2(z[0], z[1], x[k], x[k + 1], kz, kz);
-    mul2(u[0], u[1], z[0], z[1], z[0], z[1]);
-    fma2(p[0], p[1], u[0], u[1], T4 * cl, T3 * cl);
-    fma2e(p[0], p[1], u[0], u[1], T2 * cl);
-    fma2e(p[0], p[1], u[0], u[1], T1 * cl);
-    fma2e(p[0], p[1], u[0], u[1], cl);
-    mul2(y[0], y[1], z[0], z[1], p[0], p[1]);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float f = fmaf(-2.f * cl, rcp(1.f + ex2(z[e] * (2.f * LOG2E))), cl);
-      x[k + e] = u[e] <= CAP_NEAR ? y[e] : f;
     }
   }
 }
@@ -415,7 +401,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AmArgs a) {
   constexpr uint32_t TILE = tile_bytes<D>();
   constexpr int NST = ring<D>(), NBOX = D / 64;
-  constexpr bool BIASED = MODE == BIAS || MODE == BOTH;
+  constexpr bool BIASED = MODE == BIAS || MODE == BOTH, CAPPED = MODE == CAP || MODE == BOTH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -672,8 +658,8 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     const uint32_t lane_f = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t scol = tbase + lane_f + s * 128, ocol = tbase + lane_f + O_COL + s * 128;
     const float scale_log2 = a.scale * LOG2E;
-    Cap cap;
-    if (MODE == CAP) cap.init(a.scale, a.softcap);
+    Cap<MODE == BOTH> cap;
+    if (CAPPED) cap.init(a.scale, a.softcap, a.kz);
     int np = 0, no = 0, c = 0;  // tiles and items this stream has had, ring entries so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -730,20 +716,17 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         };
         auto take = [&]() {  // the row's scores, transformed and masked
           load();
-          if (MODE == CAP && !far && !cap_near(x, cap, live)) {
+          if (CAPPED && !far && !cap_near(x, cap, live)) {
             far = 1;  // for the rest of the item: such scores seldom come alone
             load();
           }
           // in a block of its own, and its numbers made there: in one with the loads, or kept
-          // through all tiles, it spills 250 bytes of the near form's registers
-          if (MODE == CAP) asm volatile("" : "+r"(far));
-          if ((MODE == BOTH && a.softcap > 0.f) || (MODE == CAP && far)) {
+          // through all tiles, it spills more of the near form's registers (254 bytes, not 216)
+          if (CAPPED) asm volatile("" : "+r"(far));
+          if (CAPPED && far) {
             float kz = a.kz, cl = a.softcap * LOG2E;
             asm volatile("" : "+f"(kz), "+f"(cl));
-            if (MODE == CAP)
-              cap_far(x, cap, 2.f * LOG2E * kz, cl);
-            else
-              cap_any(x, kz, cl);
+            cap_far(x, cap, 2.f * LOG2E * kz, cl);
           }
           if (BIASED && a.slopes)  // (BIAS always: the branch keeps the loads from spilling)
             bias_scores(x, MODE == BIAS ? scale_log2 : 1.f, slope, (float)(place - t0));
