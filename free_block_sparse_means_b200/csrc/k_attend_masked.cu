@@ -910,11 +910,11 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             }
           }
         }
-        if (live && a.lse)
-          a.lse[((int64_t)it.b * a.Hq + h) * a.Nq + qi] =
-              l == 0.f ? -INFINITY
-                       : fmaf(BIASED && a.slopes ? -a.slopes[h] : 0.f, it.lim.beyond(qi),
-                              (m - p_shift<T>()) * LN2 + logf(l));
+        if (live && a.lse) {
+          float lse = l == 0.f ? -INFINITY : (m - p_shift<T>()) * LN2 + logf(l);
+          if (BIASED && a.slopes && l != 0.f) lse = fmaf(-a.slopes[h], it.lim.beyond(qi), lse);
+          a.lse[((int64_t)it.b * a.Hq + h) * a.Nq + qi] = lse;
+        }
       }
       if (any) {
         tc::tc_fence_before();
