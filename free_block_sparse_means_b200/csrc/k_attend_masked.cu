@@ -25,15 +25,18 @@
 //
 // What bounds it: a 128 x 128 tile is 1,024 cycles of products (d = 128) and, at 16
 // exponentials a cycle, 1,024 of the multi-function unit; two streams' tiles take
-// 3,300 cycles on an SM, each unit at 0.62.  The softmax's own chain (scores out
-// of TMEM, maximum, exponentials, P back) is the longest part, so it is cut short:
-// the exponentials go ahead with the old maximum, and the product with V starts
-// on the first half of P.  16 heads x 16,384 x 16,384, d = 128: 1,820 us, 1,210 TFLOP/s.
-// Measured and not kept (same case): products issued under `lane == 0` 2,307 us;
-// a quarter of the exponentials as polynomials on the FMA pipe 2,067; a row shared
-// by two threads, 16 softmax warps 2,243; S, P and O in steps of 64 keys 2,449.
-// SOLO is bound by reading K and V: 8 x 8 key heads, 15,100 to 32,768 keys: 165 us,
-// 4.8 TB/s.
+// 4,050 cycles on an SM, the tensor pipe busy 0.51 and the multi-function unit 0.62 of
+// them by their counters.  The softmax's own chain (scores out of TMEM, maximum,
+// exponentials, P back) is the longest part, so it is cut short: the exponentials go
+// ahead with the old maximum, and the product with V starts on the first half of P.
+// 16 heads x 16,384 x 16,384, d = 128, inputs changing: 2,070 to 2,110 us at 1.74 GHz,
+// 1,050 TFLOP/s; d = 64: 1,715 us at 1.965 GHz, 640 TFLOP/s.
+// Measured and not kept (same case, on one box where this form took 1,820 us):
+// products issued under `lane == 0` 2,307 us; a quarter of the exponentials as
+// polynomials on the FMA pipe 2,067; a row shared by two threads, 16 softmax warps
+// 2,243; S, P and O in steps of 64 keys 2,449.
+// SOLO is bound by reading K and V: 8 x 8 key heads, 12,950 to 32,768 keys: 165 to 175 us
+// with the join, 4.8 TB/s.
 //
 // Masks: with causal and prefix a row sees exactly the keys below one limit,
 // which grows with the row, so a tile is skipped, partly masked or whole by
@@ -263,7 +266,7 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // (2^-23.4 relative, in exact arithmetic), with kz and the scale in its coefficients; 6
 // packed operations for two scores, none on the multi-function unit.  (Working in z takes
 // 7, as does a cap with a penalty: 2 x 16 heads x 4,097 x 4,097, d = 64, with a prefix, 272 us
-// against 265.)  Beyond, it is
+// against 267.)  Beyond, it is
 // c - 2 c / (1 + e^(2 z)), whose error is a few 2^-24 of c: near 0 that would be all of a
 // score, so each score takes the form that is exact relative to itself.
 // Z: in z, with coefficients of usual size under any cap.
@@ -720,14 +723,12 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             far = 1;  // for the rest of the item: such scores seldom come alone
             load();
           }
-          // in a block of its own, and its numbers made there: in one with the loads, or kept
-          // through all tiles, it spills more of the near form's registers (254 bytes, not 216)
+          // The compiler must not see that `far` follows from the branch above: it then makes one
+          // block of the loads and the far form, whose spills the near form pays for (2 x 16 heads
+          // x 4,097, d = 64, cap and prefix 270 -> 282 us; 24 heads x 8,192, cap and slopes 1,316 ->
+          // 1,760).
           if (CAPPED) asm volatile("" : "+r"(far));
-          if (CAPPED && far) {
-            float kz = a.kz, cl = a.softcap * LOG2E;
-            asm volatile("" : "+f"(kz), "+f"(cl));
-            cap_far(x, cap, 2.f * LOG2E * kz, cl);
-          }
+          if (CAPPED && far) cap_far(x, cap, 2.f * LOG2E * a.kz, a.softcap * LOG2E);
           if (BIASED && a.slopes)  // (BIAS always: the branch keeps the loads from spilling)
             bias_scores(x, MODE == BIAS ? scale_log2 : 1.f, slope, (float)(place - t0));
           if (part) hide(-INFINITY);
@@ -735,7 +736,10 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         const float sl2 = MODE == PLAIN ? scale_log2 : 1.f;
         uint32_t pr[32];
         float sum4[4];
-        // P of 64 keys from key K0 on.  A row that has seen nothing keeps m = -inf;
+        // P of 64 keys from key K0 on, rounded to the 16-bit type: the product takes both operands
+        // in one type.  That is half a step a probability, at random: O's error against 64 bits is
+        // 0.0019 of its size instead of the 0.0017 of its own rounding where few keys count (slopes),
+        // less where many do.  The sum takes them unrounded.  A row that has seen nothing keeps m = -inf;
         // what it adds up meanwhile is dropped with the first score it sees, or at the end.
         auto exps = [&](auto from) {
           constexpr int K0 = decltype(from)::value;

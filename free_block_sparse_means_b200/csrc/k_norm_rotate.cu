@@ -12,7 +12,8 @@
 // Bound by HBM: every row is read and written once.  A thread keeps its token
 // through a group of heads, so that the token's angles are read once for the group,
 // queries and keys alike, and has NR_HEADS rows in flight.  118,800 tokens x (24 + 24)
-// heads, d = 128: 487 us, 6.1 TB/s, 0.93 of the copy bandwidth.
+// heads, d = 128, inputs changing: 495 to 520 us, 5.7 to 6.0 TB/s, 0.87 to 0.92 of the copy
+// bandwidth (487 us on the inputs of the pass before); fp32, 40,000 tokens: 317 us, 6.3 TB/s.
 #include <cuda_fp16.h>
 
 #include "spr_internal.cuh"

@@ -6,8 +6,8 @@
 //   a handful of rows, so the bound is reading W.  A warp streams 8 rows of W
 //   per load instruction straight into the B fragments of mma.sync (16 x 8 x 16,
 //   the rows of X are A); the warps of a block split K and add up in shared memory.
-//   4 rows x 5,120 x 5,120: 16.6 us, 3.2 TB/s of weights; x 20,480: 45 us, 4.7 TB/s.
-//   (32 rows this way: 38 us at 5,120 x 5,120, the other form 29 us.)
+//   4 rows x 5,120 x 5,120: 17.6 us, 3.0 TB/s of weights; x 20,480: 46.6 us, 4.5 TB/s.
+//   (32 rows this way: 38 us at 5,120 x 5,120, the other form 22 us.)
 //
 // k_project_pair  Everything else, on the 5th-generation tensor cores.  Two CTAs
 //   of a cluster make one tile of 256 rows x bn channels (cta_group::2): each
@@ -22,13 +22,13 @@
 //   Head-major X: 64 channels of K never cross a head (dx is a multiple of 64).
 //   Rows: a tile's 128 rows are of one batch, or of several whole batches of at
 //   most 64 rows (the box of the tensor map spans them).
-//   75,600 x 5,120 x 5,120 with gate and residual: 2.6 to 3.0 ms, 1,320 to 1,500
-//   TFLOP/s; the tensor pipe is busy 0.89 of the time and the clock is at 1.44 GHz, so
-//   the power limit is the bound.  8,190 x 2,048 x 6,144 (768 tiles on 74 pairs, 10.4
-//   rounds): 141 us, 1,460 TFLOP/s.  Under `lane == 0` instead of a uniform loop the
-//   issuing thread was the bound: 3,350 and 176 us.
-//   With few stages to a tile the epilogue is the bound: 65,144 x 344 x 4,360 with silu
-//   (two operations of the multi-function unit an output) 352 us, without 271.
+//   75,600 x 5,120 x 5,120 with gate and residual, inputs changing: 3.02 to 3.14 ms at
+//   1.15 to 1.25 GHz, 1,270 to 1,310 TFLOP/s; the tensor pipe is busy 0.89 of the time at
+//   18,944 rows, so the power limit is the bound.  8,190 x 2,048 x 6,144 (768 tiles on 74
+//   pairs, 10.4 rounds): 162 to 168 us at 1.4 GHz, 1,250 TFLOP/s.  Under `lane == 0` instead
+//   of a uniform loop the issuing thread was the bound (12 % and 20 % longer).
+//   With few stages to a tile the epilogue is the bound: 65,144 x 344 x 4,360 with bias and
+//   silu (two operations of the multi-function unit an output) 390 us, without silu 334.
 //   Where tiles are too few for the SMs, K is split, the sums go to the workspace
 //   in fp32 and k_project_join adds them and does the epilogue.
 //
@@ -515,6 +515,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
                     make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             continue;
           }
+          // Each step over all 64 channels: a branch for every 8 of them cost more than
+          // the arithmetic (1,650 cycles a chunk without any activation).  Before the waits for
+          // the buffers, under which bias and gate are on their way (65,144 x 344 x 4,360 with
+          // bias 346 -> 334 us).
+          float* f = reinterpret_cast<float*>(v);
+          if (bias) each8<T>(f, bias, col, a.M, [](float x, float c) { return x + c; });
+          if (a.act != SPR_ACT_NONE)
+            with_act(a.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) f[i] = activate<decltype(act)::value>(f[i]);
+            });
+          if (gate) each8<T>(f, gate, col, a.M, [](float x, float c) { return x * c; });
           // the buffer's last store has left it
           if (tid == 0) {
             if (a.R)
@@ -533,16 +545,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PJ_THREADS, 1)
           tc::named_sync(1 + wg, 128);
           uint8_t* to = a.R || !(ny & 1) ? buf0 : buf1;
           ++ny;
-          // Each step over all 64 channels: a branch for every 8 of them cost more than
-          // the arithmetic (1,650 cycles a chunk without any activation).
-          float* f = reinterpret_cast<float*>(v);
-          if (bias) each8<T>(f, bias, col, a.M, [](float x, float c) { return x + c; });
-          if (a.act != SPR_ACT_NONE)
-            with_act(a.act, [&](auto act) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) f[i] = activate<decltype(act)::value>(f[i]);
-            });
-          if (gate) each8<T>(f, gate, col, a.M, [](float x, float c) { return x * c; });
           if (a.R) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
