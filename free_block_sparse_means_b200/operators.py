@@ -124,7 +124,7 @@ def _run(where, tensors, names, stream, call, *args):
     """Check where the tensors live (the first one decides) and make the call there."""
     index = tensors[0].get_device()
     grad = torch.is_grad_enabled()
-    dual = forward_ad._current_level >= 0
+    dual = getattr(forward_ad, "_current_level", 0) >= 0  # 0.8 us a tensor to look, so only then
     astray = None
     for i, t in enumerate(tensors):
         if t is not None:
